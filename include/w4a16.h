@@ -364,6 +364,103 @@ int w4a8_mx_gemm_plan(const uint8_t* X8, const float* xscale, const void* wp, co
 int w4a8_mx_variants(void);
 const char* w4a8_mx_variant_name(int variant);
 
+/* ---- the operators beside the product in a decoder step ------------------------------
+ * What a decoder layer around these products has to run as well: the norm that makes the
+ * fp8 rows of w4a8_gemm, low-rank adapters beside a projection, and attention over a cache
+ * that is quantized to 4 bits like the weights.  The general rules at the top hold: device
+ * pointers, asynchronous on `stream`, arguments checked on the host first, bitwise
+ * reproducible.  `dtype` is the type of every 16-bit array of the call, W4A16_DT_F16 or
+ * W4A16_DT_BF16 (W4A16_ERR_ARG otherwise); sums, norms and softmax statistics are fp32.
+ * Rows may lie apart (ld..., in elements, a multiple of 8); row starts are 16-byte aligned.
+ * What device arrays of indices say (ids, rows, lens, table) cannot be checked on the host:
+ * the kernels bring each one into range themselves, as stated below, so none of them can
+ * make a call read or write outside the buffers that it names.
+ */
+#define W4A16_DT_F16  0
+#define W4A16_DT_BF16 1
+
+/* w4a8_rmsnorm: the residual's addition, the root-mean-square norm and its 8-bit rows.
+ *   h = x + r rounded to dtype;  y = h * rsqrt(mean(h^2) + eps) * gamma;
+ *   yscale = max|y| / 448;  Y8 = E4M3 code nearest to y / yscale (ties to even)
+ *   X, R (device, in) [M][K]; R may be NULL (h = x).  gamma (device, in) [K].
+ *   H  (device, out) [M][K], may be NULL, X or R (in place).
+ *   Y8 (device, out) [M][K] bytes and yscale (device, out) fp32 [M]: X8 and xscale of
+ *      w4a8_gemm and w4a8_mx_gemm.  Y8 8-byte aligned.
+ *   Y  (device, out) [M][K], y rounded to dtype, may be NULL (w4a16_lora's X, for example).
+ * A row of zeros gets yscale 1.  A row with a NaN gets NaN codes, a row with an infinity one
+ * NaN per infinity and zeros, yscale 1 both.  Rows of bf16 whose squares pass the fp32 range
+ * are normed correctly.  8 <= K <= 65536, K % 8 == 0, eps >= 0. */
+int w4a8_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* gamma, uint16_t* H,
+                 uint8_t* Y8, float* yscale, uint16_t* Y, int M, int K, float eps, int dtype,
+                 void* stream);
+
+/* w4a16_lora: low-rank adapters of many requests beside one projection.
+ *   Y[m] = base[m] + scale[a] * (X[m] A[a]^T) B[a]^T, a = ids[m]; the product X A^T is kept
+ *   in fp32 and Y rounded once.
+ *   X (device, in) [M] rows of K, ldx apart; A (device, in) [adapters][rank][K];
+ *   B (device, in) [adapters][N][rank]; ids (device, in) int32 [M]; scale (device, in) fp32
+ *   [adapters]; base (device, in) and Y (device, out) [M] rows of N, ldy apart; Y may be
+ *   base (in place), and must not overlap it otherwise.
+ * An id below 0 or >= adapters means no adapter: Y[m] = base[m].  Any order of ids is
+ * right; rows of one adapter side by side are fastest.  K % 8 == 0, N % 8 == 0,
+ * rank % 8 == 0, rank <= 128, M <= 2^21.  The workspace (w4a16_lora_workspace_bytes; 0 for
+ * an invalid shape) is the stream's, under the rules of w4a16_gemm. */
+int w4a16_lora(const uint16_t* X, const uint16_t* A, const uint16_t* B, const int32_t* ids,
+               const float* scale, const uint16_t* base, uint16_t* Y, int M, int N, int K, int rank,
+               int adapters, int ldx, int ldy, int dtype, void* stream);
+size_t w4a16_lora_workspace_bytes(int M, int N, int K, int rank);
+
+/* The 4-bit cache of keys and values.  For each token, kv head and group of `group`
+ * channels: codes c = 0..15 and fp16 s, m, the value being m + s * c:
+ *   m = fp16(min x), s = fp16((max x - min x) / 15), c = clamp(rint((x - m) / s), 0, 15)
+ *   (0 where s = 0), x clamped to +-65504; a NaN makes its group read as NaN.
+ * cache (device) is [pages] of w4a16_kv4_page_bytes bytes, 16-byte aligned; a page holds
+ * `page` tokens of every kv head.  Bytes inside a page are laid out for the matrix
+ * instructions (csrc/kv4.h) and need no initialisation.
+ *   head 64 or 128; group 32, 64 or 128, at most head; page a multiple of 32.
+ *   table (device) int32 [batch][width]: the page of tokens page * i .. of a sequence; entries
+ *     outside 0 .. pages - 1 mean no page.  width * page <= 2^30.
+ *   rows  (device) int32 [batch + 1], ascending: sequence b's new tokens are the rows
+ *     rows[b] .. rows[b + 1] - 1 of k, v, q and out, which have `tokens` rows.
+ *   lens  (device) int32 [batch]: tokens of each sequence, the new ones included, so the last
+ *     new one is at position lens[b] - 1.
+ *   max_new: at least the most new tokens of a sequence; what a sequence has beyond is
+ *     left alone.  Values of rows outside 0 .. tokens are brought into that range.
+ * w4a16_kv4_append: quantizes the new tokens' k and v ([tokens] rows of kv_heads * head, ldk
+ *   and ldv apart) into their pages; every other token keeps its bits.  Two sequences may
+ *   share pages of the table that neither writes.  Tokens without a page, or at a negative
+ *   position, are dropped.
+ * w4a16_kv4_gather: the other way, the values of the same tokens as rows of k and v, rounded to
+ *   dtype; zeros where there is no page.  With lens = the lengths and rows their running
+ *   sums it reads whole sequences.
+ * w4a16_kv4_attention: out = softmax(scale * q k^T) v of each new token over the cached ones
+ *   (append them first): token t of position p is seen if t <= p, t > p - window
+ *   (window > 0 only) and it has a page.  q (device, in) and out (device, out): [tokens] rows
+ *   of q_heads * head, ldq and ldo apart; query head h reads kv head h / (q_heads / kv_heads).
+ *   lse (device, out) fp32 [tokens][q_heads], may be NULL: the natural logarithm of the sum
+ *   of exp(scale * q k).  A token that sees nothing gets out 0 and lse -infinity.  What the
+ *   pages hold in places that no token sees does not matter.  max_len: at least the
+ *   longest of lens (a longer one is still right, but slow).  The workspace
+ *   (w4a16_kv4_workspace_bytes; 0 for an invalid shape, and where none is needed) is the
+ *   stream's, under the rules of w4a16_gemm.
+ * w4a16_kv4_page_bytes: 0 for an invalid layout. */
+size_t w4a16_kv4_page_bytes(int kv_heads, int head, int group, int page);
+int w4a16_kv4_append(const uint16_t* k, const uint16_t* v, const int32_t* rows,
+                     const int32_t* lens, const int32_t* table, void* cache, int batch, int tokens,
+                     int max_new, int ldk, int ldv, int kv_heads, int head, int group, int page,
+                     int pages, int width, int dtype, void* stream);
+int w4a16_kv4_gather(const void* cache, const int32_t* rows, const int32_t* lens,
+                     const int32_t* table, uint16_t* k, uint16_t* v, int batch, int tokens,
+                     int max_new, int ldk, int ldv, int kv_heads, int head, int group, int page,
+                     int pages, int width, int dtype, void* stream);
+int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
+                        const int32_t* table, const void* cache, uint16_t* out, float* lse,
+                        int batch, int tokens, int max_new, int max_len, int ldq, int ldo,
+                        int q_heads, int kv_heads, int head, int group, int page, int pages,
+                        int width, int window, float scale, int dtype, void* stream);
+size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len, int q_heads,
+                                 int kv_heads, int head, int window);
+
 /* ---- calibration kernels (measurement only) ---------------------------------------
  * The achievable ceilings the GEMM's rates are set against, beside the published peaks.
  * w4a16_probe_read: one plain streaming read of `bytes` bytes at device pointer p

@@ -30,6 +30,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 _SIGS = {
     "w4a16_layout_version": (_I, []),
@@ -65,6 +66,14 @@ _SIGS = {
     "w4a8_mx_gemm_plan": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
     "w4a8_mx_variants": (_I, []),
     "w4a8_mx_variant_name": (ctypes.c_char_p, [_I]),
+    "w4a8_rmsnorm": (_I, [_P] * 7 + [_I, _I, _F, _I, _P]),
+    "w4a16_lora": (_I, [_P] * 7 + [_I] * 8 + [_P]),
+    "w4a16_lora_workspace_bytes": (_SZ, [_I] * 4),
+    "w4a16_kv4_page_bytes": (_SZ, [_I] * 4),
+    "w4a16_kv4_append": (_I, [_P] * 6 + [_I] * 12 + [_P]),
+    "w4a16_kv4_gather": (_I, [_P] * 6 + [_I] * 12 + [_P]),
+    "w4a16_kv4_attention": (_I, [_P] * 7 + [_I] * 14 + [_F, _I, _P]),
+    "w4a16_kv4_workspace_bytes": (_SZ, [_I] * 8),
     "w4a16_probe_read": (_I, [_P, _SZ, _P, _P]),
     "w4a16_probe_mfma": (_I, [_I, _I, _P, _P]),
     "w4a16_probe_mfma_flops": (ctypes.c_double, [_I, _I]),
@@ -290,6 +299,60 @@ def alloc_mx(K: int, N: int, device="cuda"):
     import torch
     return (torch.empty(K * N // 2, dtype=torch.uint8, device=device),
             torch.empty(K * N // 32, dtype=torch.uint8, device=device))
+
+
+# ---- the operators beside the product in a decoder step --------------------------------
+DT_F16, DT_BF16 = range(2)  # W4A16_DT_F16, W4A16_DT_BF16
+
+
+def w4a8_rmsnorm(X, R, gamma, H, Y8, yscale, Y, M, K, eps, dtype=DT_F16, stream=None):
+    _check("w4a8_rmsnorm", _lib.w4a8_rmsnorm(
+        _ptr(X), _ptr(R), _ptr(gamma), _ptr(H), _ptr(Y8), _ptr(yscale), _ptr(Y), M, K, eps, dtype,
+        _stream(stream)))
+
+
+def w4a16_lora(X, A, B, ids, scale, base, Y, M, N, K, rank, adapters, ldx, ldy, dtype=DT_F16,
+               stream=None):
+    _check("w4a16_lora", _lib.w4a16_lora(
+        _ptr(X), _ptr(A), _ptr(B), _ptr(ids), _ptr(scale), _ptr(base), _ptr(Y), M, N, K, rank,
+        adapters, ldx, ldy, dtype, _stream(stream)))
+
+
+def w4a16_lora_workspace_bytes(M: int, N: int, K: int, rank: int) -> int:
+    return _lib.w4a16_lora_workspace_bytes(M, N, K, rank)
+
+
+def w4a16_kv4_page_bytes(kv_heads: int, head: int, group: int, page: int) -> int:
+    return _lib.w4a16_kv4_page_bytes(kv_heads, head, group, page)
+
+
+def w4a16_kv4_append(k, v, rows, lens, table, cache, batch, tokens, max_new, ldk, ldv, kv_heads,
+                     head, group, page, pages, width, dtype=DT_F16, stream=None):
+    _check("w4a16_kv4_append", _lib.w4a16_kv4_append(
+        _ptr(k), _ptr(v), _ptr(rows), _ptr(lens), _ptr(table), _ptr(cache), batch, tokens, max_new,
+        ldk, ldv, kv_heads, head, group, page, pages, width, dtype, _stream(stream)))
+
+
+def w4a16_kv4_gather(cache, rows, lens, table, k, v, batch, tokens, max_new, ldk, ldv, kv_heads,
+                     head, group, page, pages, width, dtype=DT_F16, stream=None):
+    _check("w4a16_kv4_gather", _lib.w4a16_kv4_gather(
+        _ptr(cache), _ptr(rows), _ptr(lens), _ptr(table), _ptr(k), _ptr(v), batch, tokens, max_new,
+        ldk, ldv, kv_heads, head, group, page, pages, width, dtype, _stream(stream)))
+
+
+def w4a16_kv4_attention(q, rows, lens, table, cache, out, lse, batch, tokens, max_new, max_len,
+                        ldq, ldo, q_heads, kv_heads, head, group, page, pages, width, window,
+                        scale, dtype=DT_F16, stream=None):
+    _check("w4a16_kv4_attention", _lib.w4a16_kv4_attention(
+        _ptr(q), _ptr(rows), _ptr(lens), _ptr(table), _ptr(cache), _ptr(out), _ptr(lse), batch,
+        tokens, max_new, max_len, ldq, ldo, q_heads, kv_heads, head, group, page, pages, width,
+        window, scale, dtype, _stream(stream)))
+
+
+def w4a16_kv4_workspace_bytes(batch: int, tokens: int, max_new: int, max_len: int, q_heads: int,
+                              kv_heads: int, head: int, window: int = 0) -> int:
+    return _lib.w4a16_kv4_workspace_bytes(batch, tokens, max_new, max_len, q_heads, kv_heads, head,
+                                          window)
 
 
 # ---- calibration kernels ---------------------------------------------------------

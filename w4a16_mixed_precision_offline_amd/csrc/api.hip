@@ -811,6 +811,203 @@ int w4a8_mx_gemm(const uint8_t* X8, const float* xscale, const void* wp, const v
   return w4a8_mx_gemm_plan(X8, xscale, wp, sp, Y, M, N, K, -1, 0, stream);
 }
 
+// ---- the operators beside the product in a decoder step ----------------------------------
+namespace {
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool is_dtype(int t) { return t == W4A16_DT_F16 || t == W4A16_DT_BF16; }
+
+// Arguments shared by the cache's entry points.  Products are 64-bit: no argument that
+// passes here makes the kernels' 32-bit block and grid indices overflow.
+int check_kv4(const void* const* ptrs16, int n16, const int32_t* const* ptrs4, int batch,
+              int tokens, int max_new, int kv_heads, int head, int group, int page, int pages,
+              int width, int dtype) {
+  for (int i = 0; i < n16; ++i)
+    if (!ptrs16[i]) return W4A16_ERR_NULL;
+  for (int i = 0; i < 3; ++i)
+    if (!ptrs4[i]) return W4A16_ERR_NULL;
+  if (!is_dtype(dtype)) return W4A16_ERR_ARG;
+  if (w4a16_kv4_page_bytes(kv_heads, head, group, page) == 0) return W4A16_ERR_SHAPE;
+  if (batch < 1 || batch > 65535 || tokens < 1 || max_new < 1 || max_new > tokens || pages < 1 ||
+      width < 1 || (long long)width * page > (1LL << 30))
+    return W4A16_ERR_SHAPE;
+  for (int i = 0; i < n16; ++i)
+    if (!aligned16(ptrs16[i])) return W4A16_ERR_ALIGN;
+  for (int i = 0; i < 3; ++i)
+    if (!aligned4(ptrs4[i])) return W4A16_ERR_ALIGN;
+  return W4A16_OK;
+}
+inline bool row_stride_ok(int ld, long long width) { return ld >= width && ld % 8 == 0; }
+
+}  // namespace
+
+int w4a8_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* gamma, uint16_t* H,
+                 uint8_t* Y8, float* yscale, uint16_t* Y, int M, int K, float eps, int dtype,
+                 void* stream) {
+  if (!X || !gamma || !Y8 || !yscale) return W4A16_ERR_NULL;
+  if (!is_dtype(dtype) || !(eps >= 0.f)) return W4A16_ERR_ARG;
+  if (M <= 0 || K <= 0 || K % 8 != 0 || K > NORM_MAX_K) return W4A16_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(R) || !aligned16(gamma) || !aligned16(H) || !aligned16(Y) ||
+      (reinterpret_cast<uintptr_t>(Y8) & 7u) != 0 || !aligned4(yscale))
+    return W4A16_ERR_ALIGN;
+  int rc = check_device(nullptr);
+  if (rc) return rc;
+  return launched(launch_rmsnorm(X, R, gamma, H, Y8, yscale, Y, M, K, eps, dtype == W4A16_DT_BF16,
+                                 static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+bool lora_shape_ok(int M, int N, int K, int rank) {
+  return M > 0 && N > 0 && K > 0 && N % 8 == 0 && K % 8 == 0 && rank > 0 && rank % 8 == 0 &&
+         rank <= LORA_MAX_RANK && M <= (1 << 21) && N <= (1 << 30) && K <= (1 << 30);
+}
+}  // namespace
+
+size_t w4a16_lora_workspace_bytes(int M, int N, int K, int rank) {
+  return lora_shape_ok(M, N, K, rank) ? lora_make_plan(M, N, K, rank).floats * sizeof(float) : 0;
+}
+
+int w4a16_lora(const uint16_t* X, const uint16_t* A, const uint16_t* B, const int32_t* ids,
+               const float* scale, const uint16_t* base, uint16_t* Y, int M, int N, int K, int rank,
+               int adapters, int ldx, int ldy, int dtype, void* stream) {
+  if (!X || !A || !B || !ids || !scale || !base || !Y) return W4A16_ERR_NULL;
+  if (!is_dtype(dtype)) return W4A16_ERR_ARG;
+  if (!lora_shape_ok(M, N, K, rank) || adapters < 1 || !row_stride_ok(ldx, K) ||
+      !row_stride_ok(ldy, N))
+    return W4A16_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(base) || !aligned16(Y) ||
+      !aligned4(ids) || !aligned4(scale))
+    return W4A16_ERR_ALIGN;
+  int dev;
+  int rc = check_device(&dev);
+  if (rc) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const LoraPlan plan = lora_make_plan(M, N, K, rank);
+  int* cnt;
+  float* part;
+  if ((rc = get_workspace(dev, st, 0, plan.floats, &cnt, &part))) return rc;
+  return launched(lora_launch(plan, X, A, B, ids, scale, base, Y, part, M, N, K, rank, adapters,
+                              ldx, ldy, dtype == W4A16_DT_BF16, st));
+}
+
+size_t w4a16_kv4_page_bytes(int kv_heads, int head, int group, int page) {
+  if (kv_heads < 1 || kv_heads > 16384 || (head != 64 && head != 128) ||
+      (group != 32 && group != 64 && group != 128) || group > head || page < 32 || page % 32 != 0 ||
+      page > (1 << 20))
+    return 0;
+  return (size_t)kv_heads * (page / 32) * (32 * head + 256 * (head / group));
+}
+
+int w4a16_kv4_append(const uint16_t* k, const uint16_t* v, const int32_t* rows,
+                     const int32_t* lens, const int32_t* table, void* cache, int batch, int tokens,
+                     int max_new, int ldk, int ldv, int kv_heads, int head, int group, int page,
+                     int pages, int width, int dtype, void* stream) {
+  const void* const p16[] = {k, v, cache};
+  const int32_t* const p4[] = {rows, lens, table};
+  int rc = check_kv4(p16, 3, p4, batch, tokens, max_new, kv_heads, head, group, page, pages, width,
+                     dtype);
+  if (rc) return rc;
+  if (!row_stride_ok(ldk, (long long)kv_heads * head) ||
+      !row_stride_ok(ldv, (long long)kv_heads * head))
+    return W4A16_ERR_SHAPE;
+  if ((rc = check_device(nullptr))) return rc;
+  const Kv4CacheArgs a{k, v, rows, lens, table, static_cast<char*>(cache), batch, tokens,
+                       max_new, ldk, ldv, kv_heads, page, pages, width};
+  return launched(launch_kv4_append(a, head, head / group, dtype == W4A16_DT_BF16,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+int w4a16_kv4_gather(const void* cache, const int32_t* rows, const int32_t* lens,
+                     const int32_t* table, uint16_t* k, uint16_t* v, int batch, int tokens,
+                     int max_new, int ldk, int ldv, int kv_heads, int head, int group, int page,
+                     int pages, int width, int dtype, void* stream) {
+  const void* const p16[] = {k, v, cache};
+  const int32_t* const p4[] = {rows, lens, table};
+  int rc = check_kv4(p16, 3, p4, batch, tokens, max_new, kv_heads, head, group, page, pages, width,
+                     dtype);
+  if (rc) return rc;
+  if (!row_stride_ok(ldk, (long long)kv_heads * head) ||
+      !row_stride_ok(ldv, (long long)kv_heads * head))
+    return W4A16_ERR_SHAPE;
+  if ((rc = check_device(nullptr))) return rc;
+  const Kv4GatherArgs a{static_cast<const char*>(cache), rows, lens, table, k, v, batch, tokens,
+                        max_new, ldk, ldv, kv_heads, page, pages, width};
+  return launched(launch_kv4_gather(a, head, head / group, dtype == W4A16_DT_BF16,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+bool kv4_attend_shape_ok(int batch, int tokens, int max_new, int max_len, int q_heads,
+                         int kv_heads, int head, int window) {
+  if (batch < 1 || batch > 65535 || tokens < 1 || max_new < 1 || max_new > tokens || max_len < 1 ||
+      max_len > (1 << 30) || kv_heads < 1 || q_heads < kv_heads || q_heads > 65536 ||
+      q_heads % kv_heads != 0 || (head != 64 && head != 128) || window < 0)
+    return false;
+  if ((long long)max_new * (q_heads / kv_heads) > (1LL << 30)) return false;
+  const Kv4AttendPlan p =
+      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
+  return (long long)p.chunks * p.col_tiles <= (1LL << 30) / kv_heads / batch;
+}
+}  // namespace
+
+size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len, int q_heads,
+                                 int kv_heads, int head, int window) {
+  if (!kv4_attend_shape_ok(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window))
+    return 0;
+  return kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window).floats *
+         sizeof(float);
+}
+
+int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
+                        const int32_t* table, const void* cache, uint16_t* out, float* lse,
+                        int batch, int tokens, int max_new, int max_len, int ldq, int ldo,
+                        int q_heads, int kv_heads, int head, int group, int page, int pages,
+                        int width, int window, float scale, int dtype, void* stream) {
+  const void* const p16[] = {q, cache, out};
+  const int32_t* const p4[] = {rows, lens, table};
+  int rc = check_kv4(p16, 3, p4, batch, tokens, max_new, kv_heads, head, group, page, pages, width,
+                     dtype);
+  if (rc) return rc;
+  if (!kv4_attend_shape_ok(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window) ||
+      !row_stride_ok(ldq, (long long)q_heads * head) ||
+      !row_stride_ok(ldo, (long long)q_heads * head))
+    return W4A16_ERR_SHAPE;
+  if (!(scale > 0.f)) return W4A16_ERR_ARG;
+  if (!aligned4(lse)) return W4A16_ERR_ALIGN;
+  int dev;
+  if ((rc = check_device(&dev))) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const Kv4AttendPlan plan =
+      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
+  int* cnt;
+  float* part;
+  if ((rc = get_workspace(dev, st, 0, plan.floats, &cnt, &part))) return rc;
+  Kv4AttendArgs a{};
+  a.q = q;
+  a.rows = rows;
+  a.lens = lens;
+  a.table = table;
+  a.cache = static_cast<const char*>(cache);
+  a.out = out;
+  a.lse = lse;
+  a.part_o = part;
+  a.part_ml = part + (plan.floats / (head + 2)) * head;
+  a.batch = batch;
+  a.tokens = tokens;
+  a.max_new = max_new;
+  a.ldq = ldq;
+  a.ldo = ldo;
+  a.q_heads = q_heads;
+  a.heads = kv_heads;
+  a.page = page;
+  a.pages = pages;
+  a.width = width;
+  a.window = window;
+  a.scale = scale;
+  return launched(
+      launch_kv4_attend(plan, a, head, head / group, dtype == W4A16_DT_BF16, st));
+}
+
 // ---- calibration kernels -------------------------------------------------------------
 int w4a16_probe_read(const void* p, size_t bytes, uint32_t* out, void* stream) {
   if (!p || !out) return W4A16_ERR_NULL;

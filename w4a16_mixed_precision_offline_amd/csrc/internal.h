@@ -170,6 +170,65 @@ hipError_t tiled_launch(const TiledPlan& p, const uint16_t* X, const void* w, co
                         const float* xscale = nullptr, bool rows16 = false,
                         bool bf16_out = false);
 
+// ---- the operators beside the product in a decoder step -----------------------------
+// rmsnorm.hip: R, H and Y may be NULL
+constexpr int NORM_MAX_K = 65536;  // a row is held in registers
+hipError_t launch_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* gamma, uint16_t* H,
+                          uint8_t* Y8, float* yscale, uint16_t* Y, int M, int K, float eps, bool bf,
+                          hipStream_t st);
+
+// lora.hip
+constexpr int LORA_MAX_RANK = 128;
+struct LoraPlan {
+  int tm;               // 16-row tiles of a workgroup's tile: 1 or 4
+  int tiles;            // tiles of 16 * tm rows
+  int kslice, slices;   // X A^T: columns of K a workgroup sums, and how many such slices
+  int ncols, pieces;    // T B^T: columns of N a workgroup writes, and how many such pieces
+  size_t floats;        // workspace: the slices' T
+};
+LoraPlan lora_make_plan(int M, int N, int K, int rank);
+hipError_t lora_launch(const LoraPlan& p, const uint16_t* X, const uint16_t* A, const uint16_t* B,
+                       const int* ids, const float* scale, const uint16_t* base, uint16_t* Y,
+                       float* T, int M, int N, int K, int rank, int adapters, int ldx, int ldy,
+                       bool bf, hipStream_t st);
+
+// kv4_cache.hip, kv4_attention.hip (format in kv4.h)
+struct Kv4CacheArgs {
+  const uint16_t *k, *v;
+  const int *rows, *lens, *table;
+  char* cache;
+  int batch, tokens, max_new, ldk, ldv, heads, page, pages, width;
+};
+struct Kv4GatherArgs {
+  const char* cache;
+  const int *rows, *lens, *table;
+  uint16_t *k, *v;
+  int batch, tokens, max_new, ldk, ldv, heads, page, pages, width;
+};
+hipError_t launch_kv4_append(const Kv4CacheArgs& a, int D, int groups, bool bf, hipStream_t st);
+hipError_t launch_kv4_gather(const Kv4GatherArgs& a, int D, int groups, bool bf, hipStream_t st);
+
+struct Kv4AttendArgs {
+  const uint16_t* q;
+  const int *rows, *lens, *table;
+  const char* cache;
+  uint16_t* out;
+  float* lse;     // may be NULL
+  float *part_o, *part_ml;
+  int batch, tokens, max_new, ldq, ldo, q_heads, heads, page, pages, width, window;
+  float scale;
+  int chunk, chunks;  // tokens of the cache a workgroup covers, and how many such chunks
+  int col_tiles;      // tiles of query columns per sequence and kv head
+};
+struct Kv4AttendPlan {
+  int col_tiles, chunk, chunks;  // as in Kv4AttendArgs
+  size_t floats;      // workspace: the chunks' sums, 0 with one chunk
+};
+Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, int q_heads,
+                              int heads, int D, int window);
+hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& a, int D, int groups,
+                             bool bf, hipStream_t st);
+
 // Calibration kernels (probes.hip).
 hipError_t launch_probe_read(const void* p, size_t bytes, uint32_t* out, hipStream_t st);
 hipError_t launch_probe_mfma(int workgroups, int iters, float* out, hipStream_t st);

@@ -1,0 +1,319 @@
+// Low-rank adapters of many requests beside one projection.
+//
+//   Y[m] = base[m] + scale[a] * (X[m] A[a]^T) B[a]^T,   a = ids[m]  (none: Y[m] = base[m])
+//
+// Two products: T = X A^T has r <= 128 columns and the whole of K to sum over, Y = T B^T has
+// r to sum over and all of N to write.  So T's sum is split over K across workgroups (each
+// slice writes its fp32 part, the second kernel adds the slices in order: the same bits
+// every time, no atomics), and the second kernel is split over N.
+//
+// Rows are taken in tiles.  Of the rows of a tile that share an adapter the first is the
+// leader: a leader's products run over the whole tile (a matrix instruction's 16 columns are
+// there anyway) and only its own adapter's rows are kept.  One prompt per adapter gives
+// one leader per tile; a decode batch of different adapters gives one per row, and each
+// adapter is read once per tile, which is what bounds such a batch.
+//
+// T is held in fp32.  For the second product it goes to the matrix instruction as a sum of
+// two 16-bit numbers, hi + lo: 22 bits in fp16 (after a power of two per row that puts its
+// largest |T| in [1, 2), so that neither overflow nor underflow touches it), 16 bits in
+// bf16, whose own step is 2^-9.
+#include "internal.h"
+#include "rows16.h"
+
+namespace w4a16 {
+
+namespace {
+
+constexpr int LW = 4;  // waves of a workgroup
+
+template <bool BF>
+__device__ __forceinline__ f32x4 mfma16(const u32x4v& a, const u32x4v& b, const f32x4& c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8v, a),
+                                                   __builtin_bit_cast(bf16x8v, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, a),
+                                                  __builtin_bit_cast(half8v, b), c, 0, 0, 0);
+}
+
+// Lane l's adapter: that of row m0 + l of a tile of 16 * TM rows (-1: none).
+template <int TM>
+__device__ __forceinline__ int tile_id(const int* ids, int m0, int M, int adapters) {
+  const int lane = threadIdx.x & 63;
+  const int id = lane < 16 * TM && m0 + lane < M ? ids[m0 + lane] : -1;
+  return id >= 0 && id < adapters ? id : -1;
+}
+// The leaders a workgroup still has to serve, as a mask of the rows it may look at: all of
+// the tile (TM > 1), or row z alone, if no earlier row has its adapter (TM == 1).
+template <int TM>
+__device__ __forceinline__ uint64_t tile_todo(int id, int z) {
+  if constexpr (TM > 1) return __ballot(id >= 0);
+  const int a = __builtin_amdgcn_readlane(id, z);
+  const uint64_t same = __ballot(id == a && id >= 0);
+  return same != 0 && __builtin_ctzll(same) == z ? same : 0;
+}
+
+// T[slice][m][rp] (rp: the rank rounded up to 16) = X[m][its slice of K] A[a]^T.
+// Grid: (slices of K, tiles of 16 TM rows, TM == 1 ? leaders : 1).
+template <int TM, int RT, bool BF>
+__global__ __launch_bounds__(64 * LW) void lora_shrink_kernel(
+    const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, const int* __restrict__ ids,
+    float* __restrict__ T, int M, int K, int rank, int adapters, int ldx, int kslice) {
+  __shared__ f32x4 red[LW][RT * TM][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int r = lane & 15, g = lane >> 4;
+  const int m0 = blockIdx.y * 16 * TM;
+  const int id = tile_id<TM>(ids, m0, M, adapters);
+  uint64_t todo = tile_todo<TM>(id, blockIdx.z);
+  const int k0 = blockIdx.x * kslice;
+  const int k1 = k0 + kslice < K ? k0 + kslice : K;
+  const int rp = (rank + 15) & ~15;
+  while (todo) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    todo &= ~__ballot(id == a);
+    const uint16_t* Aa = A + (size_t)a * rank * K;
+    f32x4 acc[RT][TM];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int t = 0; t < TM; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int kk = k0 + 32 * wave; kk < k1; kk += 32 * LW) {
+      const int k = kk + 8 * g;
+      u32x4v af[RT], xf[TM];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        af[i] = u32x4v{0u, 0u, 0u, 0u};
+        if (16 * i + r < rank && k < k1)
+          af[i] = *reinterpret_cast<const u32x4v*>(Aa + (size_t)(16 * i + r) * K + k);
+      }
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        xf[t] = u32x4v{0u, 0u, 0u, 0u};
+        const int m = m0 + 16 * t + r;
+        if (m < M && k < k1)
+          xf[t] = *reinterpret_cast<const u32x4v*>(X + (size_t)m * ldx + k);
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int t = 0; t < TM; ++t) acc[i][t] = mfma16<BF>(af[i], xf[t], acc[i][t]);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int t = 0; t < TM; ++t) red[wave][i * TM + t][lane] = acc[i][t];
+    __syncthreads();
+    // lane: rows 16 i + 4 g .. + 3 of A, row m0 + 16 t + r of X
+    for (int p = wave; p < RT * TM; p += LW) {
+      f32x4 v = red[0][p][lane];
+#pragma unroll
+      for (int w = 1; w < LW; ++w) v += red[w][p][lane];
+      const int i = p / TM, t = p - i * TM;
+      const int mine = __shfl(id, 16 * t + r);
+      const int m = m0 + 16 * t + r;
+      if (mine == a && 16 * i < rp)
+        *reinterpret_cast<f32x4*>(T + ((size_t)blockIdx.x * M + m) * rp + 16 * i + 4 * g) = v;
+    }
+    __syncthreads();
+  }
+}
+
+// Y = base + scale (sum over slices of T) B^T.  A wave takes 64 columns at a time: row i of
+// matrix tile t stands for column 16 (i / 4) + 4 t + i % 4, so that a lane ends with 16
+// columns side by side.  Grid: (column pieces, tiles, TM == 1 ? leaders + 1 : 1); the last
+// z of TM == 1 copies the rows without an adapter.
+template <int TM, int KR, bool BF>
+__global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
+    const float* __restrict__ T, const uint16_t* __restrict__ B, const int* __restrict__ ids,
+    const float* __restrict__ scale, const uint16_t* base, uint16_t* Y, int M, int N, int rank,
+    int adapters, int ldy, int slices, int ncols) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int r = lane & 15, g = lane >> 4;
+  const int m0 = blockIdx.y * 16 * TM;
+  const int id = tile_id<TM>(ids, m0, M, adapters);
+  const int n0 = blockIdx.x * ncols + 64 * wave;
+  const int n1 = (int)(blockIdx.x + 1) * ncols < N ? (int)(blockIdx.x + 1) * ncols : N;
+  const bool copy = TM > 1 || blockIdx.z == 16;
+  uint64_t todo = TM == 1 && copy ? 0 : tile_todo<TM>(id, blockIdx.z);
+  if (copy && base != Y) {
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      const int m = m0 + 16 * t + r;
+      const int mine = __shfl(id, 16 * t + r);
+      if (m < M && mine < 0)
+        for (int nn = n0; nn < n1; nn += 64 * LW) {
+          const int n = nn + 16 * g;
+          const size_t at = (size_t)m * ldy + n;
+          if (n < n1)
+            *reinterpret_cast<u32x4v*>(Y + at) = *reinterpret_cast<const u32x4v*>(base + at);
+          if (n + 8 < n1)
+            *reinterpret_cast<u32x4v*>(Y + at + 8) =
+                *reinterpret_cast<const u32x4v*>(base + at + 8);
+        }
+    }
+  }
+  const int rp = (rank + 15) & ~15;
+  while (todo) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    todo &= ~__ballot(id == a);
+    const uint16_t* Ba = B + (size_t)a * rank * N;
+    const float sc = scale[a];
+    u32x4v hi[TM][KR], lo[TM][KR];
+    float up[TM];
+    bool mine[TM];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      const int m = m0 + 16 * t + r;
+      mine[t] = __shfl(id, 16 * t + r) == a;
+      float v[KR][8];
+      float top = 0.f;
+#pragma unroll
+      for (int q = 0; q < KR; ++q) {
+        const int c = 32 * q + 8 * g;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[q][e] = 0.f;
+        if (mine[t] && c < rank)
+          for (int s = 0; s < slices; ++s) {
+            const f32x4* p = reinterpret_cast<const f32x4*>(T + ((size_t)s * M + m) * rp + c);
+            const f32x4 x = p[0], y = p[1];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[q][e] += x[e];
+              v[q][4 + e] += y[e];
+            }
+          }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[q][e]));
+      }
+      float down = 1.f;
+      up[t] = sc;
+      if constexpr (!BF) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // 2^-e and 2^e, both normal; an infinite or NaN row keeps its infinities and NaN
+        int ex = (int)(__float_as_uint(top) >> 23) - 127;
+        ex = ex < -100 ? -100 : ex > 100 ? 100 : ex;
+        down = __uint_as_float((uint32_t)(127 - ex) << 23);
+        up[t] = sc * __uint_as_float((uint32_t)(127 + ex) << 23);
+      }
+#pragma unroll
+      for (int q = 0; q < KR; ++q) {
+        float h[8], l[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = v[q][e] * down;
+          h[e] = lo16<BF>(to16<BF>(x));
+          l[e] = fabsf(h[e]) < INFINITY ? x - h[e] : 0.f;
+        }
+        hi[t][q] = pack8<BF>(h);
+        lo[t][q] = pack8<BF>(l);
+      }
+    }
+    for (int nn = n0; nn < n1; nn += 64 * LW) {
+      u32x4v bf[4][KR];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int n = nn + 16 * (r >> 2) + 4 * t + (r & 3);
+#pragma unroll
+        for (int q = 0; q < KR; ++q) {
+          bf[t][q] = u32x4v{0u, 0u, 0u, 0u};
+          if (n < n1 && 32 * q + 8 * g < rank)
+            bf[t][q] = *reinterpret_cast<const u32x4v*>(Ba + (size_t)n * rank + 32 * q + 8 * g);
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < TM; ++mt) {
+        const int n = nn + 16 * g;
+        const size_t at = (size_t)(m0 + 16 * mt + r) * ldy + n;
+        const bool ok0 = mine[mt] && n < n1, ok1 = mine[mt] && n + 8 < n1;
+        u32x4v b0 = {0u, 0u, 0u, 0u}, b1 = b0;
+        if (ok0) b0 = *reinterpret_cast<const u32x4v*>(base + at);
+        if (ok1) b1 = *reinterpret_cast<const u32x4v*>(base + at + 8);
+        f32x4 acc[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < KR; ++q) {
+            acc[t] = mfma16<BF>(bf[t][q], lo[mt][q], acc[t]);
+            acc[t] = mfma16<BF>(bf[t][q], hi[mt][q], acc[t]);
+          }
+        }
+        float y[8];
+        unpack8<BF>(b0, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(up[mt], acc[e >> 2][e & 3], y[e]);
+        if (ok0) *reinterpret_cast<u32x4v*>(Y + at) = pack8<BF>(y);
+        unpack8<BF>(b1, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(up[mt], acc[2 + (e >> 2)][e & 3], y[e]);
+        if (ok1) *reinterpret_cast<u32x4v*>(Y + at + 8) = pack8<BF>(y);
+      }
+    }
+  }
+}
+
+template <int TM, bool BF>
+void shrink(dim3 grid, hipStream_t st, const uint16_t* X, const uint16_t* A, const int* ids,
+            float* T, int M, int K, int rank, int adapters, int ldx, int kslice) {
+  auto fn = rank <= 16 ? lora_shrink_kernel<TM, 1, BF>
+                       : rank <= 32 ? lora_shrink_kernel<TM, 2, BF>
+                                    : rank <= 64 ? lora_shrink_kernel<TM, 4, BF>
+                                                 : lora_shrink_kernel<TM, 8, BF>;
+  hipLaunchKernelGGL(fn, grid, dim3(64 * LW), 0, st, X, A, ids, T, M, K, rank, adapters, ldx,
+                     kslice);
+}
+template <int TM, bool BF>
+void expand(dim3 grid, hipStream_t st, const float* T, const uint16_t* B, const int* ids,
+            const float* scale, const uint16_t* base, uint16_t* Y, int M, int N, int rank,
+            int adapters, int ldy, int slices, int ncols) {
+  auto fn = rank <= 32 ? lora_expand_kernel<TM, 1, BF>
+                       : rank <= 64 ? lora_expand_kernel<TM, 2, BF> : lora_expand_kernel<TM, 4, BF>;
+  hipLaunchKernelGGL(fn, grid, dim3(64 * LW), 0, st, T, B, ids, scale, base, Y, M, N, rank,
+                     adapters, ldy, slices, ncols);
+}
+
+}  // namespace
+
+LoraPlan lora_make_plan(int M, int N, int K, int rank) {
+  LoraPlan p;
+  p.tm = M > 64 ? 4 : 1;
+  p.tiles = (M + 16 * p.tm - 1) / (16 * p.tm);
+  p.kslice = 512;
+  while ((K + p.kslice - 1) / p.kslice > 16) p.kslice *= 2;
+  p.slices = (K + p.kslice - 1) / p.kslice;
+  p.ncols = 256;
+  p.pieces = (N + p.ncols - 1) / p.ncols;
+  p.floats = (size_t)p.slices * M * ((rank + 15) / 16 * 16);
+  return p;
+}
+
+hipError_t lora_launch(const LoraPlan& p, const uint16_t* X, const uint16_t* A, const uint16_t* B,
+                       const int* ids, const float* scale, const uint16_t* base, uint16_t* Y,
+                       float* T, int M, int N, int K, int rank, int adapters, int ldx, int ldy,
+                       bool bf, hipStream_t st) {
+  const dim3 g1(p.slices, p.tiles, p.tm == 1 ? 16 : 1);
+  const dim3 g2(p.pieces, p.tiles, p.tm == 1 ? 17 : 1);
+  if (p.tm == 1) {
+    (bf ? shrink<1, true> : shrink<1, false>)(g1, st, X, A, ids, T, M, K, rank, adapters, ldx,
+                                              p.kslice);
+  } else {
+    (bf ? shrink<4, true> : shrink<4, false>)(g1, st, X, A, ids, T, M, K, rank, adapters, ldx,
+                                              p.kslice);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (p.tm == 1) {
+    (bf ? expand<1, true> : expand<1, false>)(g2, st, T, B, ids, scale, base, Y, M, N, rank,
+                                              adapters, ldy, p.slices, p.ncols);
+  } else {
+    (bf ? expand<4, true> : expand<4, false>)(g2, st, T, B, ids, scale, base, Y, M, N, rank,
+                                              adapters, ldy, p.slices, p.ncols);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace w4a16

@@ -1,0 +1,177 @@
+// Residual addition, root-mean-square norm and the 8-bit rows of the W4A8 product.
+//
+//   h = rne16(x + r),  y = h * rsqrt(mean(h^2) + eps) * g,
+//   s = max|y| / 448 (1 for a row of zeros),  y8 = e4m3(y / s)
+//
+// One workgroup holds one row in registers, so every input is read once.  Both things a row
+// has to agree on, sum(h^2) and max|h g|, come from one pass and one exchange through LDS:
+// y = inv * (h g) with inv > 0 common to the row, so max|y| = inv * max|h g| and
+// y / s = (h g) * (448 / max|h g|), which needs no norm at all.  Sums are fp32.
+//
+// bf16 rows can square past the fp32 range: a row whose sum is not finite is summed again
+// with h scaled by 2^-64, which leaves only true infinities and NaN.  They end as the
+// formula ends: a NaN makes the row's codes NaN, an infinity is a NaN among zeros, and
+// s = 1 for both.
+#include "internal.h"
+#include "rows16.h"
+
+namespace w4a16 {
+
+namespace {
+
+// max|h g| below this is taken as this (448 / max must stay finite)
+constexpr float kTinyTop = 0x1p-110f;
+
+// T threads, CH 16-byte chunks of a row in each.
+template <int T, int CH, bool BF>
+__global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4v* R,
+                                                    const u32x4v* __restrict__ gamma, u32x4v* H,
+                                                    u32x2v* __restrict__ Y8,
+                                                    float* __restrict__ yscale, u32x4v* Y, int K,
+                                                    float eps) {
+  constexpr int NW = T / 64;
+  __shared__ float red[2][NW][2];
+  const int tid = threadIdx.x;
+  const int chunks = K / 8;
+  const size_t row = (size_t)blockIdx.x * chunks;
+  u32x4v h[CH], gm[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int c = tid + j * T;
+    h[j] = u32x4v{0u, 0u, 0u, 0u};
+    gm[j] = h[j];
+    if (c < chunks) {
+      h[j] = X[row + c];
+      gm[j] = gamma[c];
+    }
+  }
+  if (R != nullptr) {
+    u32x4v r[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = tid + j * T;
+      r[j] = c < chunks ? R[row + c] : u32x4v{0u, 0u, 0u, 0u};
+    }
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      float a[8], b[8];
+      unpack8<BF>(h[j], a);
+      unpack8<BF>(r[j], b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] += b[e];
+      h[j] = pack8<BF>(a);
+    }
+  }
+  if (H != nullptr) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      const int c = tid + j * T;
+      if (c < chunks) H[row + c] = h[j];
+    }
+  }
+  // the row's sum of squares and largest |h g|, with h times `pre`
+  auto reduce = [&](float pre, int slot, float& ss, float& top) {
+    ss = 0.f;
+    top = 0.f;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      float a[8], g[8];
+      unpack8<BF>(h[j], a);
+      unpack8<BF>(gm[j], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = a[e] * pre;
+        ss = __builtin_fmaf(v, v, ss);
+        top = fmaxf(top, fabsf(v * g[e]));
+      }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      ss += __shfl_xor(ss, off);
+      top = fmaxf(top, __shfl_xor(top, off));
+    }
+    if constexpr (NW > 1) {
+      if ((tid & 63) == 0) {
+        red[slot][tid >> 6][0] = ss;
+        red[slot][tid >> 6][1] = top;
+      }
+      __syncthreads();
+      ss = red[slot][0][0];
+      top = red[slot][0][1];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) {
+        ss += red[slot][w][0];
+        top = fmaxf(top, red[slot][w][1]);
+      }
+    }
+  };
+  float ss, top, pre = 1.f;
+  reduce(1.f, 0, ss, top);
+  float inv = rsqrtf(ss / (float)K + eps);
+  if (!(ss < INFINITY)) {  // the same for the whole workgroup
+    pre = 0x1p-64f;
+    reduce(pre, 1, ss, top);
+    inv = rsqrtf(ss / (float)K);  // eps * 2^-128 is nothing beside it
+  }
+  const bool zero = top == 0.f;
+  top = fmaxf(top, kTinyTop);
+  float up = 448.f / top;
+  float s = inv * top * (1.f / 448.f);
+  if (ss != ss) up = NAN;
+  if (zero || !(s > 0.f && s < INFINITY)) s = 1.f;
+  if (tid == 0) yscale[blockIdx.x] = s;
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int c = tid + j * T;
+    if (c >= chunks) continue;
+    float a[8], g[8], y[8];
+    unpack8<BF>(h[j], a);
+    unpack8<BF>(gm[j], g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] *= pre;
+      y[e] = a[e] * g[e] * up;
+    }
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
+    Y8[row + c] = u32x2v{(uint32_t)lo, (uint32_t)hi};
+    if (Y != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = a[e] * inv * g[e];
+      Y[row + c] = pack8<BF>(y);
+    }
+  }
+}
+
+typedef void (*NormFn)(const u32x4v*, const u32x4v*, const u32x4v*, u32x4v*, u32x2v*, float*,
+                       u32x4v*, int, float);
+template <bool BF>
+NormFn norm_kernel(int threads, int ch) {
+  if (threads == 256)
+    return ch <= 1 ? rmsnorm_kernel<256, 1, BF>
+                   : ch <= 2 ? rmsnorm_kernel<256, 2, BF> : rmsnorm_kernel<256, 4, BF>;
+  return ch <= 1 ? rmsnorm_kernel<1024, 1, BF>
+                 : ch <= 2 ? rmsnorm_kernel<1024, 2, BF>
+                           : ch <= 4 ? rmsnorm_kernel<1024, 4, BF> : rmsnorm_kernel<1024, 8, BF>;
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* gamma, uint16_t* H,
+                          uint8_t* Y8, float* yscale, uint16_t* Y, int M, int K, float eps, bool bf,
+                          hipStream_t st) {
+  if (M <= 0 || K <= 0 || K % 8 != 0 || K > NORM_MAX_K) return hipErrorInvalidValue;
+  const int chunks = K / 8;
+  const int threads = chunks <= 1024 ? 256 : 1024;
+  const int ch = (chunks + threads - 1) / threads;
+  NormFn fn = bf ? norm_kernel<true>(threads, ch) : norm_kernel<false>(threads, ch);
+  hipLaunchKernelGGL(fn, dim3(M), dim3(threads), 0, st, reinterpret_cast<const u32x4v*>(X),
+                     reinterpret_cast<const u32x4v*>(R), reinterpret_cast<const u32x4v*>(gamma),
+                     reinterpret_cast<u32x4v*>(H), reinterpret_cast<u32x2v*>(Y8), yscale,
+                     reinterpret_cast<u32x4v*>(Y), K, eps);
+  return hipGetLastError();
+}
+
+}  // namespace w4a16
