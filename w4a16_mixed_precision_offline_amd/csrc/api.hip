@@ -940,7 +940,7 @@ namespace {
 bool kv4_attend_shape_ok(int batch, int tokens, int max_new, int max_len, int q_heads,
                          int kv_heads, int head, int window) {
   if (batch < 1 || batch > 65535 || tokens < 1 || max_new < 1 || max_new > tokens || max_len < 1 ||
-      max_len > (1 << 30) || kv_heads < 1 || q_heads < kv_heads || q_heads > 65536 ||
+      max_len > (1 << 30) || kv_heads < 1 || q_heads < kv_heads || q_heads > 65535 ||
       q_heads % kv_heads != 0 || (head != 64 && head != 128) || window < 0)
     return false;
   if ((long long)max_new * (q_heads / kv_heads) > (1LL << 30)) return false;

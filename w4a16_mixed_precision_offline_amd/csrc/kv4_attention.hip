@@ -12,8 +12,11 @@
 //           q is first scaled per row by a power of two into fp16's top binade, exact for
 //           every value within 2^-25 of the row's largest, so bf16 rows take the same path.
 //   softmax in powers of two.  The reference of a column moves only when a logit exceeds it
-//           by 7, then the sums so far are scaled; p = 2^(x - ref + 8) <= 2^15 is rounded to
-//           fp16 (2^-11) for the second product and summed unrounded in fp32.
+//           by 7, then the sums so far are scaled; p = 2^(x - ref + 8) <= 2^15 is summed in fp32.
+//           For the second product it is rounded to fp16 (2^-11: an eighth of bf16's own
+//           step), and for fp16 rows split into hi + lo, 22 bits, so that V's rounding is the
+//           only one beside that of the result: 1.6 to 1.3 times the error of rounding
+//           alone, at 16 more matrix instructions a block, which a stream from HBM hides.
 //   V^T p^T A = V = m_t + s_t c in fp16 (one rounding of the exact value, 2^-11), B = p, which
 //           is where K q^T left it.  Values past 65504 (a group whose s was rounded up)
 //           saturate (MODE.FP16_OVFL).
@@ -195,13 +198,9 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
   const int page_blocks = p.page / 32;
   const size_t page_bytes = (size_t)p.heads * page_blocks * kv4_block_bytes(D, NG);
   const char* head_base = p.cache + (size_t)head * page_blocks * kv4_block_bytes(D, NG);
-  for (int blk = b0 + wave; blk < b1; blk += AW) {
-    const int page = kv4_page(p.table, b, blk, page_blocks, p.width, p.pages);
-    if (page < 0) continue;
-    Block<D, NG> kv;
-    kv.load(head_base + (size_t)page * page_bytes +
-                (size_t)(blk % page_blocks) * kv4_block_bytes(D, NG),
-            lane);
+  const int* table = p.table + (size_t)b * p.width;
+
+  auto process = [&](Block<D, NG>& kv, int blk) {
     const int t0 = blk * 32;
     // logits of the lane's 8 tokens kv4_slot_token(g, e)
     float x[8];
@@ -253,18 +252,73 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) o[t] *= f;
     }
-    float pr[8];
+    float pr[8], rest[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       pr[e] = __builtin_amdgcn_exp2f(x[e] - ref + kLift);
       sum += pr[e];
     }
-    const half8v pf = __builtin_bit_cast(half8v, pack8<false>(pr));
+    const u32x4v pw = pack8<false>(pr);
+    const half8v ph = __builtin_bit_cast(half8v, pw);
+    half8v pl;
+    if constexpr (!BF) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rest[e] = pr[e] - half_at(pw, e);
+      pl = __builtin_bit_cast(half8v, pack8<false>(rest));
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int q = t * 16 / (D / NG);
-      o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(values(kv.v[t >> 2][t & 3], kv.vs[q], kv.vm[q]),
-                                                    pf, o[t], 0, 0, 0);
+      const half8v vf = values(kv.v[t >> 2][t & 3], kv.vs[q], kv.vm[q]);
+      o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, ph, o[t], 0, 0, 0);
+      if constexpr (!BF) o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl, o[t], 0, 0, 0);
+    }
+  };
+
+  // A wave's blocks b0 + wave, + AW, ...: the next block's loads are in flight while one is
+  // worked on, and its page number is fetched one block earlier still.  Blocks without a
+  // page are passed over; a load past the last block reads the last one again.
+  int blk = b0 + wave;
+  int entry = blk / page_blocks, off = blk - entry * page_blocks;
+  auto look_up = [&]() {
+    const int pg = entry < p.width && blk < b1 ? table[entry] : -1;
+    return pg >= 0 && pg < p.pages ? pg : -1;
+  };
+  auto advance = [&]() {
+    blk += AW;
+    off += AW;
+    while (off >= page_blocks) {
+      off -= page_blocks;
+      ++entry;
+    }
+  };
+  auto base_of = [&](int pg, int o_) {
+    return head_base + (size_t)(pg < 0 ? 0 : pg) * page_bytes +
+           (size_t)o_ * kv4_block_bytes(D, NG);
+  };
+  if (blk < b1) {
+    Block<D, NG> kv0, kv1;
+    int pg0 = look_up(), blk0 = blk;
+    kv0.load(base_of(pg0, off), lane);
+    advance();
+    int pg1 = look_up(), blk1 = blk, off1 = off;
+    for (;;) {
+      kv1.load(base_of(pg1, off1), lane);
+      advance();
+      int pgn = look_up(), offn = off;
+      if (pg0 >= 0) process(kv0, blk0);
+      if (blk1 >= b1) break;
+      pg0 = pgn;
+      blk0 = blk;
+      kv0.load(base_of(pg0, offn), lane);
+      advance();
+      pgn = look_up();
+      offn = off;
+      if (pg1 >= 0) process(kv1, blk1);
+      if (blk0 >= b1) break;
+      pg1 = pgn;
+      blk1 = blk;
+      off1 = offn;
     }
   }
 
@@ -315,30 +369,43 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
   }
 }
 
-// Joins the chunks of a (token, query head) in order.  Grid: (new tokens of a
-// sequence, groups of query heads, sequences); D / 4 lanes to a query head.
+// Joins the chunks of a (token, query head): one workgroup, D / 4 lanes to a chunk, so that
+// a thread's loads do not wait for each other; the lanes' sums meet in LDS in order.
+// Grid: (new tokens of a sequence, query heads, sequences).
 template <int D, bool BF>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttendArgs p) {
-  constexpr int L = D / 4;
+  constexpr int L = D / 4, NC = 256 / L;
+  __shared__ f32x4 red_o[NC][L];
+  __shared__ float red_m[NC], red_l[NC];
   saturate_fp16();
   const Kv4Seq s = kv4_seq(p.rows, p.lens, blockIdx.z, p.tokens, p.max_new);
   if ((int)blockIdx.x >= s.n) return;
-  const int qh = blockIdx.y * (256 / L) + threadIdx.x / L, c = threadIdx.x % L;
-  if (qh >= p.q_heads) return;
+  const int qh = blockIdx.y, z = threadIdx.x / L, c = threadIdx.x % L;
   const int row = s.first + blockIdx.x;
   const size_t at = (size_t)row * p.q_heads + qh, step = (size_t)p.tokens * p.q_heads;
   float m = kNone, l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < p.chunks; ++k) {
-    const float mk = p.part_ml[2 * (k * step + at)], lk = p.part_ml[2 * (k * step + at) + 1];
-    if (lk == 0.f) continue;
-    const f32x4 v = *reinterpret_cast<const f32x4*>(p.part_o + (k * step + at) * D + 4 * c);
+  auto add = [&](float mk, float lk, const f32x4& v) {
     const float next = fmaxf(m, mk);
-    const float a = __builtin_amdgcn_exp2f(m - next), z = __builtin_amdgcn_exp2f(mk - next);
+    const float a = __builtin_amdgcn_exp2f(m - next), f = __builtin_amdgcn_exp2f(mk - next);
     m = next;
-    l = l * a + lk * z;
-    o = o * a + v * z;
+    l = l * a + lk * f;
+    o = o * a + v * f;
+  };
+#pragma unroll 4
+  for (int k = z; k < p.chunks; k += NC) {
+    const float* ml = p.part_ml + 2 * (k * step + at);
+    add(ml[0], ml[1], *reinterpret_cast<const f32x4*>(p.part_o + (k * step + at) * D + 4 * c));
   }
+  red_o[z][c] = o;
+  if (c == 0) {
+    red_m[z] = m;
+    red_l[z] = l;
+  }
+  __syncthreads();
+  if (z != 0) return;
+#pragma unroll
+  for (int k = 1; k < NC; ++k) add(red_m[k], red_l[k], red_o[k][c]);
   o *= l > 0.f || l != l ? 1.f / l : 0.f;
   *reinterpret_cast<u32x2v*>(p.out + (size_t)row * p.ldo + (size_t)qh * D + 4 * c) =
       u32x2v{pack16<BF>(o[0], o[1]), pack16<BF>(o[2], o[3])};
@@ -364,7 +431,7 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
   long long span = max_len;
   if (window > 0 && span > (long long)window + 47) span = (long long)window + 47;
   const long long wgs = (long long)p.col_tiles * heads * batch;
-  long long chunks = (2048 + wgs - 1) / wgs;
+  long long chunks = (1024 + wgs - 1) / wgs;
   long long chunk = (span + chunks - 1) / chunks;
   chunk = chunk < 256 ? 256 : (chunk + 31) / 32 * 32;
   p.chunk = (int)chunk;
@@ -385,8 +452,7 @@ hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& arg
                      dim3(64 * AW), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.chunks == 1) return e;
-  const int per = 256 / (D / 4);
-  const dim3 jgrid(a.max_new, (a.q_heads + per - 1) / per, a.batch);
+  const dim3 jgrid(a.max_new, a.q_heads, a.batch);
   auto join = D == 128 ? (bf ? kv4_join_kernel<128, true> : kv4_join_kernel<128, false>)
                        : (bf ? kv4_join_kernel<64, true> : kv4_join_kernel<64, false>);
   hipLaunchKernelGGL(join, jgrid, dim3(256), 0, st, a);

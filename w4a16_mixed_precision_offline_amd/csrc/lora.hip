@@ -78,8 +78,12 @@ __global__ __launch_bounds__(64 * LW) void lora_shrink_kernel(
     for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int t = 0; t < TM; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int kk = k0 + 32 * wave; kk < k1; kk += 32 * LW) {
+    // a wave's part of the slice lies together: 16 rows' 64-byte pieces of one load and the
+    // next share cache lines
+    const int kw = kslice / LW;
+    const int ka = k0 + kw * wave, kb = ka + kw < k1 ? ka + kw : k1;
+#pragma unroll 4
+    for (int kk = ka; kk < kb; kk += 32) {
       const int k = kk + 8 * g;
       u32x4v af[RT], xf[TM];
 #pragma unroll
@@ -129,6 +133,8 @@ __global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
     const float* __restrict__ T, const uint16_t* __restrict__ B, const int* __restrict__ ids,
     const float* __restrict__ scale, const uint16_t* base, uint16_t* Y, int M, int N, int rank,
     int adapters, int ldy, int slices, int ncols) {
+  __shared__ u32x4v split[2][TM][KR][64];  // T's tile as hi and lo operands
+  __shared__ float ups[16 * TM];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int r = lane & 15, g = lane >> 4;
@@ -161,13 +167,10 @@ __global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
     todo &= ~__ballot(id == a);
     const uint16_t* Ba = B + (size_t)a * rank * N;
     const float sc = scale[a];
-    u32x4v hi[TM][KR], lo[TM][KR];
-    float up[TM];
-    bool mine[TM];
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
+    // a wave sums one row tile's slices and splits it; all waves take all tiles from LDS
+    for (int t = wave; t < TM; t += LW) {
       const int m = m0 + 16 * t + r;
-      mine[t] = __shfl(id, 16 * t + r) == a;
+      const bool mine = __shfl(id, 16 * t + r) == a;
       float v[KR][8];
       float top = 0.f;
 #pragma unroll
@@ -175,21 +178,23 @@ __global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
         const int c = 32 * q + 8 * g;
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[q][e] = 0.f;
-        if (mine[t] && c < rank)
+        if (mine && c < rank) {
+          const float* p = T + (size_t)m * rp + c;
+#pragma unroll 8
           for (int s = 0; s < slices; ++s) {
-            const f32x4* p = reinterpret_cast<const f32x4*>(T + ((size_t)s * M + m) * rp + c);
-            const f32x4 x = p[0], y = p[1];
+            const f32x4* at = reinterpret_cast<const f32x4*>(p + (size_t)s * M * rp);
+            const f32x4 x = at[0], y = at[1];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               v[q][e] += x[e];
               v[q][4 + e] += y[e];
             }
           }
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[q][e]));
       }
-      float down = 1.f;
-      up[t] = sc;
+      float down = 1.f, up = sc;
       if constexpr (!BF) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -197,8 +202,9 @@ __global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
         int ex = (int)(__float_as_uint(top) >> 23) - 127;
         ex = ex < -100 ? -100 : ex > 100 ? 100 : ex;
         down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        up[t] = sc * __uint_as_float((uint32_t)(127 + ex) << 23);
+        up = sc * __uint_as_float((uint32_t)(127 + ex) << 23);
       }
+      if (g == 0) ups[16 * t + r] = mine ? up : 0.f;
 #pragma unroll
       for (int q = 0; q < KR; ++q) {
         float h[8], l[8];
@@ -208,12 +214,20 @@ __global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
           h[e] = lo16<BF>(to16<BF>(x));
           l[e] = fabsf(h[e]) < INFINITY ? x - h[e] : 0.f;
         }
-        hi[t][q] = pack8<BF>(h);
-        lo[t][q] = pack8<BF>(l);
+        split[0][t][q][lane] = pack8<BF>(h);
+        split[1][t][q][lane] = pack8<BF>(l);
       }
     }
+    __syncthreads();
+    float up[TM];
+    bool mine[TM];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      up[t] = ups[16 * t + r];
+      mine[t] = __shfl(id, 16 * t + r) == a;
+    }
     for (int nn = n0; nn < n1; nn += 64 * LW) {
-      u32x4v bf[4][KR];
+      u32x4v bf[4][KR], b0[TM], b1[TM];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int n = nn + 16 * (r >> 2) + 4 * t + (r & 3);
@@ -224,35 +238,41 @@ __global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
             bf[t][q] = *reinterpret_cast<const u32x4v*>(Ba + (size_t)n * rank + 32 * q + 8 * g);
         }
       }
+      const int n = nn + 16 * g;
 #pragma unroll
       for (int mt = 0; mt < TM; ++mt) {
-        const int n = nn + 16 * g;
         const size_t at = (size_t)(m0 + 16 * mt + r) * ldy + n;
-        const bool ok0 = mine[mt] && n < n1, ok1 = mine[mt] && n + 8 < n1;
-        u32x4v b0 = {0u, 0u, 0u, 0u}, b1 = b0;
-        if (ok0) b0 = *reinterpret_cast<const u32x4v*>(base + at);
-        if (ok1) b1 = *reinterpret_cast<const u32x4v*>(base + at + 8);
+        b0[mt] = b1[mt] = u32x4v{0u, 0u, 0u, 0u};
+        if (mine[mt] && n < n1) b0[mt] = *reinterpret_cast<const u32x4v*>(base + at);
+        if (mine[mt] && n + 8 < n1) b1[mt] = *reinterpret_cast<const u32x4v*>(base + at + 8);
+      }
+#pragma unroll
+      for (int mt = 0; mt < TM; ++mt) {
+        const size_t at = (size_t)(m0 + 16 * mt + r) * ldy + n;
         f32x4 acc[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int q = 0; q < KR; ++q) {
-            acc[t] = mfma16<BF>(bf[t][q], lo[mt][q], acc[t]);
-            acc[t] = mfma16<BF>(bf[t][q], hi[mt][q], acc[t]);
+        for (int q = 0; q < KR; ++q) {
+          const u32x4v hi = split[0][mt][q][lane], lo = split[1][mt][q][lane];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            acc[t] = mfma16<BF>(bf[t][q], lo, acc[t]);
+            acc[t] = mfma16<BF>(bf[t][q], hi, acc[t]);
           }
         }
         float y[8];
-        unpack8<BF>(b0, y);
+        unpack8<BF>(b0[mt], y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(up[mt], acc[e >> 2][e & 3], y[e]);
-        if (ok0) *reinterpret_cast<u32x4v*>(Y + at) = pack8<BF>(y);
-        unpack8<BF>(b1, y);
+        if (mine[mt] && n < n1) *reinterpret_cast<u32x4v*>(Y + at) = pack8<BF>(y);
+        unpack8<BF>(b1[mt], y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(up[mt], acc[2 + (e >> 2)][e & 3], y[e]);
-        if (ok1) *reinterpret_cast<u32x4v*>(Y + at + 8) = pack8<BF>(y);
+        if (mine[mt] && n + 8 < n1) *reinterpret_cast<u32x4v*>(Y + at + 8) = pack8<BF>(y);
       }
     }
+    __syncthreads();
   }
 }
 
@@ -282,10 +302,16 @@ LoraPlan lora_make_plan(int M, int N, int K, int rank) {
   LoraPlan p;
   p.tm = M > 64 ? 4 : 1;
   p.tiles = (M + 16 * p.tm - 1) / (16 * p.tm);
+  // workgroups: one per (leader, slice); M leaders are the most there can be of few rows
+  const int leaders = p.tm == 1 ? M : p.tiles;
   p.kslice = 512;
-  while ((K + p.kslice - 1) / p.kslice > 16) p.kslice *= 2;
+  while (p.kslice < K && ((long long)leaders * ((K + p.kslice - 1) / p.kslice) > 512 ||
+                          (K + p.kslice - 1) / p.kslice > 16))
+    p.kslice *= 2;
   p.slices = (K + p.kslice - 1) / p.kslice;
   p.ncols = 256;
+  while (p.ncols < 1024 && (long long)p.tiles * ((N + 2 * p.ncols - 1) / (2 * p.ncols)) >= 512)
+    p.ncols *= 2;
   p.pieces = (N + p.ncols - 1) / p.ncols;
   p.floats = (size_t)p.slices * M * ((rank + 15) / 16 * 16);
   return p;
