@@ -946,7 +946,8 @@ bool kv4_attend_shape_ok(int batch, int tokens, int max_new, int max_len, int q_
   if ((long long)max_new * (q_heads / kv_heads) > (1LL << 30)) return false;
   const Kv4AttendPlan p =
       kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
-  return (long long)p.chunks * p.col_tiles <= (1LL << 30) / kv_heads / batch;
+  return (long long)p.col_tiles <= (1LL << 30) / kv_heads / batch &&
+         p.counters * sizeof(int) <= W4A16_WS_COUNTER_BYTES;
 }
 }  // namespace
 
@@ -954,8 +955,9 @@ size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len
                                  int kv_heads, int head, int window) {
   if (!kv4_attend_shape_ok(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window))
     return 0;
-  return kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window).floats *
-         sizeof(float);
+  const Kv4AttendPlan p =
+      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
+  return (p.counters + 63) / 64 * 64 * sizeof(int) + p.floats * sizeof(float);
 }
 
 int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
@@ -981,7 +983,7 @@ int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* l
       kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
   int* cnt;
   float* part;
-  if ((rc = get_workspace(dev, st, 0, plan.floats, &cnt, &part))) return rc;
+  if ((rc = get_workspace(dev, st, plan.counters, plan.floats, &cnt, &part))) return rc;
   Kv4AttendArgs a{};
   a.q = q;
   a.rows = rows;
@@ -991,7 +993,8 @@ int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* l
   a.out = out;
   a.lse = lse;
   a.part_o = part;
-  a.part_ml = part + (plan.floats / (head + 2)) * head;
+  a.part_ml = part + (size_t)plan.slots * plan.cols * head;
+  a.counters = cnt;
   a.batch = batch;
   a.tokens = tokens;
   a.max_new = max_new;
@@ -1002,7 +1005,7 @@ int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* l
   a.page = page;
   a.pages = pages;
   a.width = width;
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 1 << 30;  // no cached token lies further back
   a.scale = scale;
   return launched(
       launch_kv4_attend(plan, a, head, head / group, dtype == W4A16_DT_BF16, st));

@@ -215,19 +215,24 @@ struct Kv4AttendArgs {
   uint16_t* out;
   float* lse;     // may be NULL
   float *part_o, *part_ml;
+  int* counters;  // zero at rest, one per tile
   int batch, tokens, max_new, ldq, ldo, q_heads, heads, page, pages, width, window;
   float scale;
-  int chunk, chunks;  // tokens of the cache a workgroup covers, and how many such chunks
   int col_tiles;      // tiles of query columns per sequence and kv head
+  int target;         // chunks to cut all tiles' blocks into
+  int chunk, chunks;  // least blocks of a chunk, most chunks of a tile
+  int slots, tiles;   // workgroups and tiles that the launch has room for
 };
 struct Kv4AttendPlan {
-  int col_tiles, chunk, chunks;  // as in Kv4AttendArgs
-  size_t floats;      // workspace: the chunks' sums, 0 with one chunk
+  int cols;           // columns of a tile: 8, 16 (kv4_attention.hip) or 128 (kv4_prefill.hip)
+  int col_tiles, target, chunk, chunks, slots, tiles;  // as in Kv4AttendArgs; slots 0: no chunks
+  size_t floats, counters;  // workspace
 };
 Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, int q_heads,
                               int heads, int D, int window);
 hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& a, int D, int groups,
                              bool bf, hipStream_t st);
+hipError_t launch_kv4_prefill(const Kv4AttendArgs& a, int D, int groups, bool bf, hipStream_t st);
 
 // Calibration kernels (probes.hip).
 hipError_t launch_probe_read(const void* p, size_t bytes, uint32_t* out, hipStream_t st);

@@ -27,56 +27,27 @@
 // the tokens that no column sees: what a page holds there may be anything.
 // A column that sees nothing gives 0 and a log-sum of -infinity.
 //
-// Few columns and long contexts: the token axis is cut into chunks, one workgroup each,
-// whose sums a second kernel joins in order.
-#include "kv4.h"
+// The blocks of all tiles are cut into equal stripes, one for each of the workgroups that
+// the card holds at once; the sums of a tile that stripes share are joined in order.
+#include "kv4_attend.h"
 
 namespace w4a16 {
 
 namespace {
 
 constexpr int AW = 4;              // waves of a workgroup, which share its blocks
-constexpr float kLazy = 7.f;       // how far a logit may exceed the reference
-constexpr float kLift = 8.f;       // p is held times 2^8
-constexpr float kNone = -1e30f;    // reference of a column that has seen nothing
 
-// fp16 results past 65504 become 65504 instead of infinity, for the rest of the wave
-__device__ __forceinline__ void saturate_fp16() {
-  __builtin_amdgcn_s_setreg((0 << 11) | (23 << 6) | 1, 1);  // MODE, bit 23, one bit
-}
-
-__device__ __forceinline__ half2v as_half2(uint32_t w) { return __builtin_bit_cast(half2v, w); }
-__device__ __forceinline__ uint32_t as_word(half2v h) { return __builtin_bit_cast(uint32_t, h); }
-
-// the eight codes of a word as fp16 subnormals, channels 2, 3, 6, 7 times 16
-__device__ __forceinline__ half8v codes_subnormal(uint32_t w) {
-  const uint32_t v = w >> 8;
-  return __builtin_bit_cast(half8v, u32x4v{w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu,
-                                           v & 0x00F000F0u});
-}
-// the eight values m + s c of a word; s and m of its tokens in the same order
-__device__ __forceinline__ half8v values(uint32_t w, const u32x4v& s, const u32x4v& m) {
-  const uint32_t v = w >> 8;
-  const half2v one = {(_Float16)-1024.f, (_Float16)-1024.f};
-  const half2v up = {(_Float16)0.0625f, (_Float16)0.0625f};
-  const half2v off = {(_Float16)-64.f, (_Float16)-64.f};
-  const half2v c0 = as_half2((w & 0x000F000Fu) | 0x64006400u) + one;
-  const half2v c1 = __builtin_elementwise_fma(as_half2((w & 0x00F000F0u) | 0x64006400u), up, off);
-  const half2v c2 = as_half2((v & 0x000F000Fu) | 0x64006400u) + one;
-  const half2v c3 = __builtin_elementwise_fma(as_half2((v & 0x00F000F0u) | 0x64006400u), up, off);
-  return __builtin_bit_cast(
-      half8v, u32x4v{as_word(__builtin_elementwise_fma(c0, as_half2(s[0]), as_half2(m[0]))),
-                     as_word(__builtin_elementwise_fma(c1, as_half2(s[1]), as_half2(m[1]))),
-                     as_word(__builtin_elementwise_fma(c2, as_half2(s[2]), as_half2(m[2]))),
-                     as_word(__builtin_elementwise_fma(c3, as_half2(s[3]), as_half2(m[3])))});
-}
+constexpr int kPrefillColumns = 64;  // columns of a sequence above which tiles have 128
 
 // One block of 32 tokens of one kv head in a wave's registers.
-template <int D, int NG>
+// With tiles of 8 columns a lane needs K's s and m for 4 tokens only (those of tile r / 8).
+template <int D, int NG, int TC>
 struct Block {
+  typedef uint32_t kparam __attribute__((ext_vector_type(TC / 4)));
   uint32_t k[2][D / 32];
   u32x4v v[D / 64];
-  u32x4v ks[NG], km[NG], vs[NG], vm[NG];
+  kparam ks[NG], km[NG];
+  u32x4v vs[NG], vm[NG];
 
   __device__ __forceinline__ void load(const char* base, int lane) {
     const int g = lane >> 4;
@@ -96,57 +67,150 @@ struct Block {
     for (int h = 0; h < D / 64; ++h)
       v[h] = *reinterpret_cast<const u32x4v*>(base + 16 * D + (h * 64 + lane) * 16);
     const char* par = base + 32 * D + 16 * g;
+    const char* kpar = par + (TC == 8 ? lane & 8 : 0);
 #pragma unroll
     for (int q = 0; q < NG; ++q) {
-      ks[q] = *reinterpret_cast<const u32x4v*>(par + 128 * q);
-      km[q] = *reinterpret_cast<const u32x4v*>(par + 128 * q + 64);
+      ks[q] = *reinterpret_cast<const kparam*>(kpar + 128 * q);
+      km[q] = *reinterpret_cast<const kparam*>(kpar + 128 * q + 64);
       vs[q] = *reinterpret_cast<const u32x4v*>(par + 128 * (NG + q));
       vm[q] = *reinterpret_cast<const u32x4v*>(par + 128 * (NG + q) + 64);
     }
   }
 };
 
-__device__ __forceinline__ float half_at(const u32x4v& v, int e) {
+template <class V>
+__device__ __forceinline__ float half_at(const V& v, int e) {
   return e & 1 ? hi16<false>(v[e >> 1]) : lo16<false>(v[e >> 1]);
 }
+// the value of lane l ^ 8 (lanes of 16 turned by 8)
+__device__ __forceinline__ uint32_t swap8(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, false);
+}
 
-// Grid: chunks x column tiles x kv heads x sequences, chunks fastest.
-template <int D, int NG, bool BF>
-__global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
+// Workgroups on different XCDs hand their sums over with relaxed agent-scope accesses, which
+// are coherent across the L2s by themselves; what orders them is that all of a workgroup's
+// stores have completed (s_waitcnt) before it counts itself in.
+__device__ __forceinline__ void put8(float* p, float a, float b) {
+  const uint64_t v = (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void get8(const float* p, float& a, float& b) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<uint64_t*>(const_cast<float*>(p)),
+                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  a = __uint_as_float((uint32_t)v);
+  b = __uint_as_float((uint32_t)(v >> 32));
+}
+__device__ __forceinline__ void get16(const float* p, f32x4& x) {
+  float a, b, c, d;
+  get8(p, a, b);
+  get8(p + 2, c, d);
+  x = f32x4{a, b, c, d};
+}
+
+// TC: columns of a tile, 16, or 8 where a sequence has no more than 8.  With 8, columns 8..15
+// of the matrix instructions serve the same columns again: K q^T leaves tile 0's tokens in
+// lanes r < 8 and tile 1's in the others, so each logit is worked on once, and V^T p^T
+// takes p's upper part from lanes r < 8 and its lower part (fp16 rows) from the others.
+template <int D, int NG, int TC, bool BF>
+__global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p) {
   constexpr int J = D / 32, JG = J / NG, NT = D / 16;
+  constexpr int E = TC / 2;       // logits of a lane in a block
   __shared__ f32x4 red_o[AW][NT][64];
-  __shared__ float red_m[AW][16], red_l[AW][16];
+  __shared__ float red_ml[8][8][2];  // [wave][column], or [part][column] of the last join
+  __shared__ int arrived;
   saturate_fp16();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int r = lane & 15, g = lane >> 4;
-  unsigned id = blockIdx.x;
-  const int chunk = id % p.chunks;
-  id /= p.chunks;
-  const int tile = id % p.col_tiles;
-  id /= p.col_tiles;
-  const int head = id % p.heads, b = id / p.heads;
   const int ratio = p.q_heads / p.heads;
-  const Kv4Seq s = kv4_seq(p.rows, p.lens, b, p.tokens, p.max_new);
-  const int i0 = tile * 16 / ratio;               // first and last new token of the tile
-  if (i0 >= s.n) return;
-  const int i1 = (tile * 16 + 15) / ratio < s.n - 1 ? (tile * 16 + 15) / ratio : s.n - 1;
-  const int from = s.len - s.n;
-  const int col = tile * 16 + r, ci = col / ratio;
-  const bool live = ci < s.n;
+  Kv4Stripes<TC> stripes;
+  typename Kv4Stripes<TC>::Lane lanes;
+  uint32_t pos = 0, stop = 1;
+  if (p.slots) {
+    lanes = stripes.init(p, ratio);
+    pos = blockIdx.x * stripes.stripe;
+    stop = pos + stripes.stripe < stripes.total ? pos + stripes.stripe : stripes.total;
+  }
+  for (bool again = false; pos < stop; again = true) {
+  Kv4Seq seq;
+  int b, head, tile, span = 1;
+  uint32_t u0 = 0, r0 = 0, r1 = 1;  // this stripe's part of the tile: blocks [r0, r1)
+  if (p.slots) {
+    // fetched again (from cache) for a further tile rather than held in registers
+    if (again && p.batch <= 64) lanes = stripes.fetch(p, 0, ratio);
+    stripes.find(p, pos, ratio, lanes, seq, b, head, tile, span, u0);
+    u0 += stripes.lead;
+    r0 = pos > u0 ? pos - u0 : 0;
+    pos = u0 - stripes.lead + stripes.tile_size(span);
+    if (stop <= u0) break;  // it has the lead of a tile only
+    r1 = stop - u0 < (uint32_t)span ? stop - u0 : (uint32_t)span;
+    if (r0 >= r1) continue;  // what rounds a tile up to whole stripes
+  } else {
+    Kv4Place w;
+    if (!kv4_place_whole(p, w)) return;
+    seq = w.s;
+    b = w.b;
+    head = w.head;
+    tile = w.tile;
+    pos = 1;
+  }
+  const Kv4Range rg = kv4_range<TC>(p, seq, tile, ratio, r0, r1 == (uint32_t)span ? -1 : (int)r1);
+  if (rg.i0 >= seq.n) return;  // a tile past the sequence's last, in a launch without stripes
+  const int rc = TC == 8 ? r & 7 : r;
+  const int col = tile * TC + rc, ci = col / ratio;
+  const bool live = ci < seq.n;
   const int qh = head * ratio + col % ratio;
-  const int row = s.first + (live ? ci : 0);
+  const int row = seq.first + (live ? ci : 0);
   // tokens seen: column [first, last], any column [lo, hi), every column [all_lo, all_hi)
-  const int last = live ? from + ci : -1;
+  const int lo = rg.lo, hi = rg.hi;
+  const int last = live ? rg.from + ci : -1;
   const int first = p.window > 0 ? last - p.window + 1 : 0;
-  const int hi = from + i1 + 1;
-  int lo = p.window > 0 ? from + i0 - p.window + 1 : 0;
-  lo = lo < 0 ? 0 : lo;
-  const int all_hi = from + i0 + 1;
-  const int all_lo = p.window > 0 ? from + i1 - p.window + 1 : 0;
+  const int all_hi = rg.from + rg.i0 + 1;
+  const int all_lo = p.window > 0 ? rg.from + rg.i1 - p.window + 1 : 0;
+
+  const int page_blocks = p.page / 32;
+  const size_t page_bytes = (size_t)p.heads * page_blocks * kv4_block_bytes(D, NG);
+  const char* head_base = p.cache + (size_t)head * page_blocks * kv4_block_bytes(D, NG);
+  const int* table = p.table + (size_t)b * p.width;
+
+  // A wave's blocks blk0 + wave, + AW, ...: the next block's loads are in flight while one is
+  // worked on, and its page number is fetched one block earlier still, before those loads,
+  // so that no wait for it waits for them.  Blocks without a page are passed over; a load
+  // past the last block reads some block of the table.
+  const int b1 = rg.blk1;
+  int blk = rg.blk0 + wave;
+  int entry = blk / page_blocks, off = blk - entry * page_blocks;
+  auto look_up = [&]() { return table[entry < p.width ? entry : p.width - 1]; };
+  auto valid = [&](int pg) { return pg >= 0 && pg < p.pages; };
+  auto advance = [&]() {
+    blk += AW;
+    off += AW;
+    while (off >= page_blocks) {
+      off -= page_blocks;
+      ++entry;
+    }
+  };
+  auto base_of = [&](int pg, int o_) {
+    pg = __builtin_amdgcn_readfirstlane(pg);
+    return head_base + (size_t)(valid(pg) ? pg : 0) * page_bytes +
+           (size_t)o_ * kv4_block_bytes(D, NG);
+  };
+  Block<D, NG, TC> kv0, kv1;
+  const bool any = blk < b1;
+  int pg0 = 0, pg1 = 0, blk0 = blk, blk1 = 0, off1 = 0;
+  if (any) {
+    pg0 = look_up();
+    const int off0 = off;
+    advance();
+    pg1 = look_up();
+    blk1 = blk;
+    off1 = off;
+    kv0.load(base_of(pg0, off0), lane);
+  }
 
   // q, scaled, and its sums per group of channels (times 2^-24, the codes' unit)
-  half8v qf[J];
+  half8v qf[TC == 8 ? 2 : 1][J];
   float qsum[NG], cf;
   {
     float f[J][8], top = 0.f;
@@ -160,8 +224,7 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
     }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    int d = 15 - ((int)(__float_as_uint(top) >> 23) - 127);
-    d = top == 0.f ? 0 : d < -112 ? -112 : d > 100 ? 100 : d;
+    const int d = query_exponent(top);
     const float up = __builtin_ldexpf(1.f, d);
 #pragma unroll
     for (int q = 0; q < NG; ++q) qsum[q] = 0.f;
@@ -174,7 +237,14 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
         qsum[j / JG] += x;
         h[e] = e & 2 ? x * 0.0625f : x;
       }
-      qf[j] = __builtin_bit_cast(half8v, pack8<false>(h));
+      const u32x4v x = pack8<false>(h);
+      if constexpr (TC == 8) {
+        const u32x4v zero = {0u, 0u, 0u, 0u};
+        qf[0][j] = __builtin_bit_cast(half8v, r < 8 ? x : zero);
+        qf[1][j] = __builtin_bit_cast(half8v, r < 8 ? zero : x);
+      } else {
+        qf[0][j] = __builtin_bit_cast(half8v, x);
+      }
     }
 #pragma unroll
     for (int q = 0; q < NG; ++q) {
@@ -188,33 +258,27 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
   f32x4 o[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float ref = kNone, sum = 0.f;
+  float ref = kKv4None, sum = 0.f;
 
-  // this workgroup's blocks: its chunk of [lo, hi), the last chunk taking what is left
-  const int b0 = lo / 32 + chunk * (p.chunk / 32);
-  const int end = (hi + 31) / 32;
-  const int b1 = chunk == p.chunks - 1 || b0 + p.chunk / 32 > end ? end
-                                                                           : b0 + p.chunk / 32;
-  const int page_blocks = p.page / 32;
-  const size_t page_bytes = (size_t)p.heads * page_blocks * kv4_block_bytes(D, NG);
-  const char* head_base = p.cache + (size_t)head * page_blocks * kv4_block_bytes(D, NG);
-  const int* table = p.table + (size_t)b * p.width;
-
-  auto process = [&](Block<D, NG>& kv, int blk) {
+  auto process = [&](Block<D, NG, TC>& kv, int blk) {
     const int t0 = blk * 32;
-    // logits of the lane's 8 tokens kv4_slot_token(g, e)
-    float x[8];
+    // logits of the lane's tokens: kv4_slot_token(g, e), or with TC == 8 the four of tile r / 8
+    float x[E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    for (int e = 0; e < E; ++e) x[e] = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < E / 4; ++t)
 #pragma unroll
       for (int q = 0; q < NG; ++q) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < JG; ++j)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_subnormal(kv.k[t][q * JG + j]),
-                                                       qf[q * JG + j], acc, 0, 0, 0);
+        for (int j = q * JG; j < (q + 1) * JG; ++j) {
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_subnormal(kv.k[t][j]), qf[0][j], acc,
+                                                       0, 0, 0);
+          if constexpr (TC == 8)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_subnormal(kv.k[1][j]), qf[1][j],
+                                                         acc, 0, 0, 0);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = 4 * t + i;
@@ -223,12 +287,16 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
         }
       }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= cf;
+    for (int e = 0; e < E; ++e) x[e] *= cf;
     if (t0 < all_lo || t0 + 32 > all_hi) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int pos = t0 + (TC == 8 ? 4 * g + e + 2 * (r & 8) : kv4_slot_token(g, e));
+        if (pos < first || pos > last) x[e] = -INFINITY;
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int pos = t0 + kv4_slot_token(g, e);
-        if (pos < first || pos > last) x[e] = -INFINITY;
         if (pos < lo || pos >= hi) {
 #pragma unroll
           for (int q = 0; q < NG; ++q) {
@@ -241,8 +309,9 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
     }
     float top = x[0];
 #pragma unroll
-    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-    if (__ballot(top > ref + kLazy) != 0) {
+    for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
+    if (__ballot(top > ref + kKv4Lazy) != 0) {
+      if constexpr (TC == 8) top = fmaxf(top, __uint_as_float(swap8(__float_as_uint(top))));
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float next = fmaxf(ref, top);
@@ -252,210 +321,287 @@ __global__ __launch_bounds__(64 * AW) void kv4_attend_kernel(Kv4AttendArgs p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) o[t] *= f;
     }
-    float pr[8], rest[8];
+    float pr[E];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      pr[e] = __builtin_amdgcn_exp2f(x[e] - ref + kLift);
+    for (int e = 0; e < E; ++e) {
+      pr[e] = __builtin_amdgcn_exp2f(x[e] - ref + kKv4Lift);
       sum += pr[e];
     }
-    const u32x4v pw = pack8<false>(pr);
-    const half8v ph = __builtin_bit_cast(half8v, pw);
-    half8v pl;
+    half8v ph, pl;
+    uint32_t hw[E / 2], lw[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) hw[e / 2] = pack16<false>(pr[e], pr[e + 1]);
     if constexpr (!BF) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) rest[e] = pr[e] - half_at(pw, e);
-      pl = __builtin_bit_cast(half8v, pack8<false>(rest));
+      for (int e = 0; e < E; e += 2)
+        lw[e / 2] = pack16<false>(pr[e] - lo16<false>(hw[e / 2]), pr[e + 1] - hi16<false>(hw[e / 2]));
+    }
+    if constexpr (TC == 8) {
+      // lanes r < 8 get tile 1's upper parts, the others tile 0's lower parts
+      uint32_t got[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) got[i] = swap8(BF ? hw[i] : r < 8 ? lw[i] : hw[i]);
+      if constexpr (BF)
+        ph = __builtin_bit_cast(half8v, u32x4v{hw[0], hw[1], got[0], got[1]});
+      else
+        ph = __builtin_bit_cast(half8v, u32x4v{r < 8 ? hw[0] : got[0], r < 8 ? hw[1] : got[1],
+                                               r < 8 ? got[0] : lw[0], r < 8 ? got[1] : lw[1]});
+    } else {
+      ph = __builtin_bit_cast(half8v, u32x4v{hw[0], hw[1], hw[2], hw[3]});
+      if constexpr (!BF) pl = __builtin_bit_cast(half8v, u32x4v{lw[0], lw[1], lw[2], lw[3]});
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int q = t * 16 / (D / NG);
       const half8v vf = values(kv.v[t >> 2][t & 3], kv.vs[q], kv.vm[q]);
       o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, ph, o[t], 0, 0, 0);
-      if constexpr (!BF) o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl, o[t], 0, 0, 0);
+      if constexpr (!BF && TC == 16)
+        o[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pl, o[t], 0, 0, 0);
     }
   };
 
-  // A wave's blocks b0 + wave, + AW, ...: the next block's loads are in flight while one is
-  // worked on, and its page number is fetched one block earlier still.  Blocks without a
-  // page are passed over; a load past the last block reads the last one again.
-  int blk = b0 + wave;
-  int entry = blk / page_blocks, off = blk - entry * page_blocks;
-  auto look_up = [&]() {
-    const int pg = entry < p.width && blk < b1 ? table[entry] : -1;
-    return pg >= 0 && pg < p.pages ? pg : -1;
-  };
-  auto advance = [&]() {
-    blk += AW;
-    off += AW;
-    while (off >= page_blocks) {
-      off -= page_blocks;
-      ++entry;
-    }
-  };
-  auto base_of = [&](int pg, int o_) {
-    return head_base + (size_t)(pg < 0 ? 0 : pg) * page_bytes +
-           (size_t)o_ * kv4_block_bytes(D, NG);
-  };
-  if (blk < b1) {
-    Block<D, NG> kv0, kv1;
-    int pg0 = look_up(), blk0 = blk;
-    kv0.load(base_of(pg0, off), lane);
-    advance();
-    int pg1 = look_up(), blk1 = blk, off1 = off;
+  if (any) {
     for (;;) {
-      kv1.load(base_of(pg1, off1), lane);
       advance();
       int pgn = look_up(), offn = off;
-      if (pg0 >= 0) process(kv0, blk0);
+      kv1.load(base_of(pg1, off1), lane);
+      if (valid(pg0)) process(kv0, blk0);
       if (blk1 >= b1) break;
       pg0 = pgn;
       blk0 = blk;
-      kv0.load(base_of(pg0, offn), lane);
       advance();
       pgn = look_up();
+      kv0.load(base_of(pg0, offn), lane);
       offn = off;
-      if (pg1 >= 0) process(kv1, blk1);
+      if (valid(pg1)) process(kv1, blk1);
       if (blk0 >= b1) break;
       pg1 = pgn;
       blk1 = blk;
       off1 = offn;
     }
   }
-
-  // join the waves
   sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);
-#pragma unroll
-  for (int t = 0; t < NT; ++t) red_o[wave][t][lane] = o[t];
-  if (g == 0) {
-    red_m[wave][r] = ref;
-    red_l[wave][r] = sum;
-  }
-  __syncthreads();
-  float m = kNone, l = 0.f, f[AW];
-#pragma unroll
-  for (int w = 0; w < AW; ++w) m = fmaxf(m, red_m[w][r]);
-#pragma unroll
-  for (int w = 0; w < AW; ++w) {
-    f[w] = __builtin_amdgcn_exp2f(red_m[w][r] - m);
-    l += f[w] * red_l[w][r];
-  }
-  if (!live) return;
-  const size_t at = (size_t)row * p.q_heads + qh;
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-#pragma unroll
-  for (int k = 0; k < NT / AW; ++k) {
-    const int t = wave + AW * k;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < AW; ++w) v += red_o[w][t][lane] * f[w];
-    if (p.chunks > 1) {
-      *reinterpret_cast<f32x4*>(
-          p.part_o + ((size_t)chunk * p.tokens * p.q_heads + at) * D + 16 * t + 4 * g) = v;
-    } else {
-      v *= inv;
-      *reinterpret_cast<u32x2v*>(p.out + (size_t)row * p.ldo + (size_t)qh * D + 16 * t + 4 * g) =
-          u32x2v{pack16<BF>(v[0], v[1]), pack16<BF>(v[2], v[3])};
-    }
-  }
-  if (wave == 0 && g == 0) {
-    if (p.chunks > 1) {
-      float* ml = p.part_ml + 2 * ((size_t)chunk * p.tokens * p.q_heads + at);
-      ml[0] = m;
-      ml[1] = l;
-    } else if (p.lse != nullptr) {
-      p.lse[at] = (m + log2f(l) - kLift) * 0.6931471805599453f;
-    }
-  }
-}
+  if constexpr (TC == 8) sum += __uint_as_float(swap8(__float_as_uint(sum)));
 
-// Joins the chunks of a (token, query head): one workgroup, D / 4 lanes to a chunk, so that
-// a thread's loads do not wait for each other; the lanes' sums meet in LDS in order.
-// Grid: (new tokens of a sequence, query heads, sequences).
-template <int D, bool BF>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttendArgs p) {
-  constexpr int L = D / 4, NC = 256 / L;
-  __shared__ f32x4 red_o[NC][L];
-  __shared__ float red_m[NC], red_l[NC];
-  saturate_fp16();
-  const Kv4Seq s = kv4_seq(p.rows, p.lens, blockIdx.z, p.tokens, p.max_new);
-  if ((int)blockIdx.x >= s.n) return;
-  const int qh = blockIdx.y, z = threadIdx.x / L, c = threadIdx.x % L;
-  const int row = s.first + blockIdx.x;
-  const size_t at = (size_t)row * p.q_heads + qh, step = (size_t)p.tokens * p.q_heads;
-  float m = kNone, l = 0.f;
-  f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  auto add = [&](float mk, float lk, const f32x4& v) {
-    const float next = fmaxf(m, mk);
-    const float a = __builtin_amdgcn_exp2f(m - next), f = __builtin_amdgcn_exp2f(mk - next);
-    m = next;
-    l = l * a + lk * f;
-    o = o * a + v * f;
-  };
-#pragma unroll 4
-  for (int k = z; k < p.chunks; k += NC) {
-    const float* ml = p.part_ml + 2 * (k * step + at);
-    add(ml[0], ml[1], *reinterpret_cast<const f32x4*>(p.part_o + (k * step + at) * D + 4 * c));
-  }
-  red_o[z][c] = o;
-  if (c == 0) {
-    red_m[z] = m;
-    red_l[z] = l;
-  }
-  __syncthreads();
-  if (z != 0) return;
+  // joins the waves: the tile's reference and sum, and rows 16 (wave + AW k) .. of its o
+  float m, l;
+  f32x4 v[NT / AW];
+  auto join = [&]() {
 #pragma unroll
-  for (int k = 1; k < NC; ++k) add(red_m[k], red_l[k], red_o[k][c]);
-  o *= l > 0.f || l != l ? 1.f / l : 0.f;
-  *reinterpret_cast<u32x2v*>(p.out + (size_t)row * p.ldo + (size_t)qh * D + 4 * c) =
-      u32x2v{pack16<BF>(o[0], o[1]), pack16<BF>(o[2], o[3])};
-  if (c == 0 && p.lse != nullptr) p.lse[at] = (m + log2f(l) - kLift) * 0.6931471805599453f;
+    for (int t = 0; t < NT; ++t) red_o[wave][t][lane] = o[t];
+    if (g == 0) {
+      red_ml[wave][r & 7][r >> 3] = ref;
+      red_ml[AW + wave][r & 7][r >> 3] = sum;
+    }
+    __syncthreads();
+    m = kKv4None;
+    l = 0.f;
+    float f[AW];
+#pragma unroll
+    for (int i = 0; i < AW; ++i) m = fmaxf(m, red_ml[i][r & 7][r >> 3]);
+#pragma unroll
+    for (int i = 0; i < AW; ++i) {
+      f[i] = __builtin_amdgcn_exp2f(red_ml[i][r & 7][r >> 3] - m);
+      l += f[i] * red_ml[AW + i][r & 7][r >> 3];
+    }
+#pragma unroll
+    for (int k = 0; k < NT / AW; ++k) {
+      v[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < AW; ++i) {
+        f32x4 x = red_o[i][wave + AW * k][lane];
+        if constexpr (TC == 8 && !BF) x += red_o[i][wave + AW * k][lane ^ 8];
+        v[k] += x * f[i];
+      }
+    }
+  };
+  join();
+  const bool mine = live && r < TC;
+  if (r0 == 0 && r1 == (uint32_t)span) {
+    if (mine) {
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+      for (int k = 0; k < NT / AW; ++k) {
+        v[k] *= inv;
+        *reinterpret_cast<u32x2v*>(p.out + (size_t)row * p.ldo + (size_t)qh * D +
+                                   16 * (wave + AW * k) + 4 * g) =
+            u32x2v{pack16<BF>(v[k][0], v[k][1]), pack16<BF>(v[k][2], v[k][3])};
+      }
+      if (wave == 0 && g == 0 && p.lse != nullptr)
+        p.lse[(size_t)row * p.q_heads + qh] = (m + log2f(l) - kKv4Lift) * 0.6931471805599453f;
+    }
+    __syncthreads();
+    continue;
+  }
+  // A shared tile: the sums go to the workspace ([column][D], and m, l per column), slot
+  // 2 w + 1 for the stripe w in which the tile starts, 2 w for the others.  The last
+  // workgroup to arrive joins them, in the order of the stripes.
+  const uint32_t w0 = u0 / stripes.stripe, w1 = (u0 + span - 1) / stripes.stripe;
+  {
+    const size_t slot = 2 * blockIdx.x + (blockIdx.x == w0);
+    if (mine) {
+#pragma unroll
+      for (int k = 0; k < NT / AW; ++k) {
+        float* at = p.part_o + (slot * TC + rc) * D + 16 * (wave + AW * k) + 4 * g;
+        put8(at, v[k][0], v[k][1]);
+        put8(at + 2, v[k][2], v[k][3]);
+      }
+      if (wave == 0 && g == 0) put8(p.part_ml + (slot * TC + rc) * 2, m, l);
+    }
+  }
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0)
+    arrived = __hip_atomic_fetch_add(p.counters + w0, 1, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const bool last_one = arrived == (int)(w1 - w0);
+  __syncthreads();
+  if (!last_one) continue;
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  if (threadIdx.x == 0)
+    __hip_atomic_store(p.counters + w0, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // Eight columns at a time: a thread takes 4 channels of one of them from every `parts`-th
+  // stripe, and the parts meet in LDS (fewer columns: more parts).
+  constexpr int NL = D / 4;
+  static_assert(8 * NL <= AW * NT * 64 && 8 * NL <= 64 * AW, "the parts fit");
+  f32x4* sums = &red_o[0][0][0];         // [z][NL]
+  const int z = threadIdx.x / NL, c4 = threadIdx.x % NL;
+#pragma unroll 1
+  for (int c8 = 0; c8 < TC; c8 += 8) {
+    const int cols = (seq.n * ratio - tile * TC) - c8;  // live columns, of the eight and on
+    if (cols <= 0) break;
+    const int shift = cols > 4 ? 3 : cols > 2 ? 2 : cols > 1 ? 1 : 0, parts = 8 >> shift;
+    const int i = z & ((1 << shift) - 1);
+    f32x4 so = {0.f, 0.f, 0.f, 0.f};
+    float sm = kKv4None, sl = 0.f;
+    if (z < 8 && i < cols) {
+      // eight stripes' loads in flight; past the last one its own again, with weight 0
+      for (uint32_t k0 = w0 + (z >> shift); k0 <= w1; k0 += 8 * parts) {
+        f32x4 x[8];
+        float cm[8], cl[8], next = sm;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t k = k0 + j * parts <= w1 ? k0 + j * parts : w1;
+          const size_t slot = (size_t)2 * k + (k == w0);
+          get16(p.part_o + (slot * TC + c8 + i) * D + 4 * c4, x[j]);
+          get8(p.part_ml + (slot * TC + c8 + i) * 2, cm[j], cl[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) next = fmaxf(next, cm[j]);
+        const float fa = __builtin_amdgcn_exp2f(sm - next);
+        sm = next;
+        sl *= fa;
+        so *= fa;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (k0 + j * parts > w1) break;
+          const float fb = __builtin_amdgcn_exp2f(cm[j] - next);
+          sl += cl[j] * fb;
+          so += x[j] * fb;
+        }
+      }
+      sums[z * NL + c4] = so;
+      if (c4 == 0) {
+        red_ml[z][0][0] = sm;
+        red_ml[z][0][1] = sl;
+      }
+    }
+    __syncthreads();
+    if (z < (1 << shift) && i < cols) {
+      float tm = kKv4None, tl = 0.f;
+      f32x4 to = {0.f, 0.f, 0.f, 0.f};
+      for (int k = z; k < 8; k += 1 << shift) tm = fmaxf(tm, red_ml[k][0][0]);
+      for (int k = z; k < 8; k += 1 << shift) {
+        const float f = __builtin_amdgcn_exp2f(red_ml[k][0][0] - tm);
+        tl += f * red_ml[k][0][1];
+        to += sums[k * NL + c4] * f;
+      }
+      to *= tl > 0.f || tl != tl ? 1.f / tl : 0.f;
+      const int tc = tile * TC + c8 + i;
+      const size_t trow = seq.first + tc / ratio;
+      const int th = head * ratio + tc % ratio;
+      *reinterpret_cast<u32x2v*>(p.out + trow * p.ldo + (size_t)th * D + 4 * c4) =
+          u32x2v{pack16<BF>(to[0], to[1]), pack16<BF>(to[2], to[3])};
+      if (c4 == 0 && p.lse != nullptr)
+        p.lse[trow * p.q_heads + th] = (tm + log2f(tl) - kKv4Lift) * 0.6931471805599453f;
+    }
+    __syncthreads();
+  }
+  }
 }
 
 typedef void (*AttendFn)(Kv4AttendArgs);
-template <bool BF>
+template <int TC, bool BF>
 AttendFn attend_kernel(int D, int groups) {
   if (D == 128)
-    return groups == 1 ? kv4_attend_kernel<128, 1, BF>
-                       : groups == 2 ? kv4_attend_kernel<128, 2, BF> : kv4_attend_kernel<128, 4, BF>;
-  return groups == 1 ? kv4_attend_kernel<64, 1, BF> : kv4_attend_kernel<64, 2, BF>;
+    return groups == 1 ? kv4_attend_kernel<128, 1, TC, BF>
+                       : groups == 2 ? kv4_attend_kernel<128, 2, TC, BF>
+                                     : kv4_attend_kernel<128, 4, TC, BF>;
+  return groups == 1 ? kv4_attend_kernel<64, 1, TC, BF> : kv4_attend_kernel<64, 2, TC, BF>;
 }
 
 }  // namespace
 
 Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, int q_heads,
                               int heads, int D, int window) {
-  Kv4AttendPlan p;
-  p.col_tiles = (int)(((long long)max_new * (q_heads / heads) + 15) / 16);
-  // tokens any tile can see: the window of its first token up to its last
-  long long span = max_len;
-  if (window > 0 && span > (long long)window + 47) span = (long long)window + 47;
-  const long long wgs = (long long)p.col_tiles * heads * batch;
-  long long chunks = (1024 + wgs - 1) / wgs;
-  long long chunk = (span + chunks - 1) / chunks;
-  chunk = chunk < 256 ? 256 : (chunk + 31) / 32 * 32;
-  p.chunk = (int)chunk;
-  p.chunks = (int)((span + chunk - 1) / chunk);
-  if (p.chunks < 1) p.chunks = 1;
-  p.floats = p.chunks > 1 ? (size_t)p.chunks * tokens * q_heads * (D + 2) : 0;
+  Kv4AttendPlan p{};
+  const int ratio = q_heads / heads;
+  const long long columns = (long long)max_new * ratio;
+  p.cols = columns <= 8 ? 8 : columns <= kPrefillColumns ? 16 : 128;
+  p.col_tiles = (int)((columns + p.cols - 1) / p.cols);
+  // tiles there can be: each sequence rounds up, and rows are not shared
+  long long tiles = ((long long)tokens * ratio + p.cols - 1) / p.cols + batch;
+  if (tiles > (long long)batch * p.col_tiles) tiles = (long long)batch * p.col_tiles;
+  tiles *= heads;
+  // blocks a tile can see: the window of its first token up to its last
+  long long span = ((long long)max_len + 31) / 32;
+  if (window > 0 && span > ((long long)window + p.cols / ratio + 1) / 32 + 2)
+    span = ((long long)window + p.cols / ratio + 1) / 32 + 2;
+  if (p.cols == 128) {
+    p.target = 512;
+    p.chunk = 16;
+    p.chunks = (int)((span + p.chunk - 1) / p.chunk);
+    if (p.chunks <= 1 || tiles >= p.target || batch > 1024) {
+      p.chunks = 1;
+      return p;  // enough tiles by themselves
+    }
+    long long slots = p.target + tiles;
+    if (slots > tiles * p.chunks) slots = tiles * p.chunks;
+    p.slots = (int)slots;
+    p.tiles = (int)tiles;
+  } else {
+    p.chunk = 8;
+    long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
+    if (batch > 1024 || stripes <= tiles) return p;
+    if (stripes > 512) stripes = 512;
+    p.target = (int)stripes;
+    p.slots = 2 * (int)stripes;
+    p.counters = (size_t)stripes;
+  }
+  p.floats = (size_t)p.slots * p.cols * (D + 2);
   return p;
 }
 
 hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& args, int D, int groups,
                              bool bf, hipStream_t st) {
   Kv4AttendArgs a = args;
+  a.col_tiles = plan.col_tiles;
+  a.target = plan.target;
   a.chunk = plan.chunk;
   a.chunks = plan.chunks;
-  a.col_tiles = plan.col_tiles;
-  const dim3 grid((unsigned)plan.chunks * plan.col_tiles * a.heads * a.batch);
-  hipLaunchKernelGGL(bf ? attend_kernel<true>(D, groups) : attend_kernel<false>(D, groups), grid,
-                     dim3(64 * AW), 0, st, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || plan.chunks == 1) return e;
-  const dim3 jgrid(a.max_new, a.q_heads, a.batch);
-  auto join = D == 128 ? (bf ? kv4_join_kernel<128, true> : kv4_join_kernel<128, false>)
-                       : (bf ? kv4_join_kernel<64, true> : kv4_join_kernel<64, false>);
-  hipLaunchKernelGGL(join, jgrid, dim3(256), 0, st, a);
+  a.slots = plan.slots;
+  a.tiles = plan.tiles;
+  if (plan.cols == 128) return launch_kv4_prefill(a, D, groups, bf, st);
+  const long long units = ((long long)a.heads * a.batch + 7) / 8 * 8;
+  const unsigned grid = plan.slots ? plan.target : (unsigned)(units * plan.col_tiles);
+  const AttendFn fn = plan.cols == 8
+                          ? (bf ? attend_kernel<8, true>(D, groups) : attend_kernel<8, false>(D, groups))
+                          : (bf ? attend_kernel<16, true>(D, groups)
+                                : attend_kernel<16, false>(D, groups));
+  hipLaunchKernelGGL(fn, dim3(grid), dim3(64 * AW), 0, st, a);
   return hipGetLastError();
 }
 
