@@ -184,7 +184,8 @@ struct LoraPlan {
   int tiles;            // tiles of 16 * tm rows
   int kslice, slices;   // X A^T: columns of K a workgroup sums, and how many such slices
   int ncols, pieces;    // T B^T: columns of N a workgroup writes, and how many such pieces
-  size_t floats;        // workspace: the slices' T
+  size_t floats;        // workspace: the slices' T, then (tm > 1) the split sums and ups
+  size_t split;             // operands of the split sums
 };
 LoraPlan lora_make_plan(int M, int N, int K, int rank);
 hipError_t lora_launch(const LoraPlan& p, const uint16_t* X, const uint16_t* A, const uint16_t* B,

@@ -87,27 +87,6 @@ __device__ __forceinline__ uint32_t swap8(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, false);
 }
 
-// Workgroups on different XCDs hand their sums over with relaxed agent-scope accesses, which
-// are coherent across the L2s by themselves; what orders them is that all of a workgroup's
-// stores have completed (s_waitcnt) before it counts itself in.
-__device__ __forceinline__ void put8(float* p, float a, float b) {
-  const uint64_t v = (uint64_t)__float_as_uint(b) << 32 | __float_as_uint(a);
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), v, __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void get8(const float* p, float& a, float& b) {
-  const uint64_t v = __hip_atomic_load(reinterpret_cast<uint64_t*>(const_cast<float*>(p)),
-                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  a = __uint_as_float((uint32_t)v);
-  b = __uint_as_float((uint32_t)(v >> 32));
-}
-__device__ __forceinline__ void get16(const float* p, f32x4& x) {
-  float a, b, c, d;
-  get8(p, a, b);
-  get8(p + 2, c, d);
-  x = f32x4{a, b, c, d};
-}
-
 // TC: columns of a tile, 16, or 8 where a sequence has no more than 8.  With 8, columns 8..15
 // of the matrix instructions serve the same columns again: K q^T leaves tile 0's tokens in
 // lanes r < 8 and tile 1's in the others, so each logit is worked on once, and V^T p^T

@@ -63,12 +63,31 @@ __global__ __launch_bounds__(64) void kv4_append_kernel(Kv4CacheArgs p) {
   const uint16_t* src = is_v ? p.v : p.k;
   const size_t ld = is_v ? p.ldv : p.ldk;
   uint16_t* params = reinterpret_cast<uint16_t*>(block + 32 * D + (is_v ? 128 * NG : 0));
+  // V's words: 8 channels of a lane, the tokens of lane group tg; those that also hold other
+  // tokens are fetched while the new ones are worked on
+  const int oct = lane >> 2, tg = lane & 3;
+  uint32_t* vdst = reinterpret_cast<uint32_t*>(block + 16 * D);
+  uint32_t old[8], mask = 0;
+  if (is_v && oct < D / 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int pos = blk * 32 + kv4_slot_token(tg, e);
+      if (pos >= start && pos < s.len) mask |= 15u << (4 * nib_pos(e));
+    }
+    if (mask != 0 && mask != 0xFFFFFFFFu) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) old[e] = vdst[v_word(8 * oct + e, tg)];
+    }
+  }
   uint32_t word[2][J];
   bool fresh[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int pos = blk * 32 + 16 * t + r;
     fresh[t] = pos >= start && pos < s.len;
+#pragma unroll
+    for (int j = 0; j < J; ++j) word[t][j] = 0;
+    if (__ballot(fresh[t]) == 0) continue;
     u32x4v x[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -106,17 +125,29 @@ __global__ __launch_bounds__(64) void kv4_append_kernel(Kv4CacheArgs p) {
         at[0] = __builtin_bit_cast(uint16_t, sh);
         at[32] = __builtin_bit_cast(uint16_t, mh);
       }
+      // (x - m) / s rounded: a product with 1 / s is off by less than 3e-6 of a code, so only
+      // where one lies closer to a half than that the quotient itself has to decide
+      const float inv = sc > 0.f ? __builtin_amdgcn_rcpf(sc) : 0.f;
+      bool close = false;
 #pragma unroll
-      for (int j = 0; j < JG; ++j) {
-        uint32_t w = 0;
+      for (int j = 0; j < JG; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          // the quotient itself, not a product with 1 / s: codes at a half go by the formula
-          float c = sc > 0.f ? __builtin_rintf((f[j][e] - m) / sc) : 0.f;
-          c = fminf(fmaxf(c, 0.f), 15.f);
-          w |= (uint32_t)(int)c << (4 * nib_pos(e));
+          const float c = (f[j][e] - m) * inv, n = __builtin_rintf(c);
+          close |= fabsf(c - n) > 0.49999f;
+          word[t][q * JG + j] |= (uint32_t)(int)fminf(fmaxf(n, 0.f), 15.f) << (4 * nib_pos(e));
         }
-        word[t][q * JG + j] = w;
+      if (__ballot(close) != 0) {
+#pragma unroll
+        for (int j = 0; j < JG; ++j) {
+          uint32_t w = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float c = sc > 0.f ? __builtin_rintf((f[j][e] - m) / sc) : 0.f;
+            w |= (uint32_t)(int)fminf(fmaxf(c, 0.f), 15.f) << (4 * nib_pos(e));
+          }
+          word[t][q * JG + j] = w;
+        }
       }
     }
   }
@@ -139,24 +170,15 @@ __global__ __launch_bounds__(64) void kv4_append_kernel(Kv4CacheArgs p) {
 #pragma unroll
     for (int j = 0; j < J; ++j) words[16 * t + r][4 * j + g] = word[t][j];
   __syncthreads();
-  const int oct = lane >> 2, tg = lane & 3;  // 8 channels, the tokens of lane group tg
-  if (oct >= D / 8) return;
-  uint32_t w[8], mask = 0;
+  if (mask == 0) return;  // also the lanes past D / 8
+  uint32_t w[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int t = kv4_slot_token(tg, e);
-    w[nib_pos(e)] = words[t][oct];
-    const int pos = blk * 32 + t;
-    if (pos >= start && pos < s.len) mask |= 15u << (4 * nib_pos(e));
-  }
-  if (mask == 0) return;
+  for (int e = 0; e < 8; ++e) w[nib_pos(e)] = words[kv4_slot_token(tg, e)][oct];
   transpose_nibbles(w);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(block + 16 * D);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    uint32_t* at = dst + v_word(8 * oct + e, tg);
     const uint32_t x = w[nib_pos(e)];
-    *at = mask == 0xFFFFFFFFu ? x : (*at & ~mask) | (x & mask);
+    vdst[v_word(8 * oct + e, tg)] = mask == 0xFFFFFFFFu ? x : (old[e] & ~mask) | (x & mask);
   }
 }
 

@@ -185,13 +185,13 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
   auto unpack = [&](Stage<D, NG>& st, int blk, int pg) {
     constexpr int W = D / 32;
     const int t0 = blk * 32, g = lane >> 4, r = lane & 15;
-    if (!valid(blk, pg)) return;  // nobody looks at it
     // what no column sees may be anything: its s and m become 0
-    if (t0 < rg.lo || t0 + 32 > rg.hi) {
+    const bool ok = valid(blk, pg);
+    if (!ok || t0 < rg.lo || t0 + 32 > rg.hi) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int pos = t0 + kv4_slot_token(g, e);
-        if (pos < rg.lo || pos >= rg.hi) {
+        if (!ok || pos < rg.lo || pos >= rg.hi) {
           const uint32_t keep = e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
           for (int i = 0; i < Piece<D, NG>::GH; ++i) {
@@ -223,45 +223,55 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
     }
   };
 
-  auto process = [&](const Stage<D, NG>& st, int i_blk, int t0) {
-    constexpr int NC = NG > 1 ? NG : 2, JC = J / NC;  // chains of the product, two at least
-    f32x16 zero;
+  constexpr bool AHEAD = NG * D <= 256;  // registers for two blocks at once
+  constexpr int NC = NG, JC = J / NC;
+  f32x16 zero;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) zero[i] = 0.f;
-    half8v kf[J];
-    const half8v mf = __builtin_bit_cast(half8v, st.m[i_blk][lane]);
+  for (int i = 0; i < 16; ++i) zero[i] = 0.f;
+
+  // The work on a block is cut where the matrix unit and the vector unit change turns, so
+  // that one block's products run beside another's exponentials:
+  //   load_k, product   x' = m (sum q), acc = c q
+  //   logits            x = x' + s acc, masked; the largest; the reference moved if need be
+  //   weights           p, their sum, p in fp16
+  //   load_v, gather    o += V^T p
+  half8v kf[J], mf, vf[2][CT], pb[2];
+  f32x16 acc[NC], x;
+  auto load_k = [&](const Stage<D, NG>& st, int i_blk) {
+    mf = __builtin_bit_cast(half8v, st.m[i_blk][lane]);
 #pragma unroll
     for (int j = 0; j < J; ++j)
       kf[j] = __builtin_bit_cast(half8v, st.k[i_blk][j / NC + j % NC * JC][lane]);
-    __builtin_amdgcn_sched_barrier(0);
-    f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_f16(mf, qm, zero, 0, 0, 0);
-    f32x16 acc[NC];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      acc[j % NC] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-          kf[j], qf[j / NC + j % NC * JC], j < NC ? zero : acc[j % NC], 0, 0, 0);
-#pragma unroll
-    for (int q = 0; q < NG; ++q)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const f32x4 s = *reinterpret_cast<const f32x4*>(&st.s[i_blk][q][8 * k + 4 * h]);
-#pragma unroll
-        for (int i = 4 * k; i < 4 * k + 4; ++i) {
-          if constexpr (NG == 1) x[i] = __builtin_fmaf(s[i & 3], acc[0][i] + acc[1][i], x[i]);
-          else x[i] = __builtin_fmaf(s[i & 3], acc[q][i], x[i]);
-        }
-      }
-    half8v vf[2][CT];
+  };
+  auto load_v = [&](const Stage<D, NG>& st, int i_blk) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int t = 0; t < CT; ++t) vf[s][t] = __builtin_bit_cast(half8v, st.v[i_blk][s][t][lane]);
-    __builtin_amdgcn_sched_barrier(0);
-    if (t0 < all_lo || t0 + 32 > all_hi) {
+  };
+  auto product = [&](f32x16& y) {
+    y = __builtin_amdgcn_mfma_f32_32x32x16_f16(mf, qm, zero, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      acc[j % NC] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+          kf[j], qf[j / NC + j % NC * JC], j < NC ? zero : acc[j % NC], 0, 0, 0);
+  };
+  auto scale = [&](const Stage<D, NG>& st, int i_blk) {
+#pragma unroll
+    for (int q = 0; q < NC; ++q)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const f32x4 s = *reinterpret_cast<const f32x4*>(&st.s[i_blk][q][8 * k + 4 * h]);
+#pragma unroll
+        for (int i = 4 * k; i < 4 * k + 4; ++i) x[i] = __builtin_fmaf(s[i & 3], acc[q][i], x[i]);
+      }
+  };
+  auto logits = [&](int t0, bool ok) {
+    if (!ok || t0 < all_lo || t0 + 32 > all_hi) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int pos = t0 + 4 * h + 8 * (i >> 2) + (i & 3);
-        if (pos < first || pos > last) x[i] = -INFINITY;
+        if (!ok || pos < first || pos > last) x[i] = -INFINITY;
       }
     }
     float top = x[0];
@@ -277,14 +287,15 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
 #pragma unroll
       for (int t = 0; t < CT; ++t) o[t] *= f;
     }
+  };
+  auto weights = [&](const f32x16& y) {
     const float base = kKv4Lift - ref;
     float pr[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      pr[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], cf, base));
+      pr[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[i], cf, base));
       sum += pr[i];
     }
-    half8v pb[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       pb[s] = __builtin_bit_cast(
@@ -292,11 +303,23 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
                          pack16<false>(pr[4 * s + 2], pr[4 * s + 3]),
                          pack16<false>(pr[4 * s + 8], pr[4 * s + 9]),
                          pack16<false>(pr[4 * s + 10], pr[4 * s + 11])});
+  };
+  auto gather = [&]() {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int t = 0; t < CT; ++t)
         o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[s][t], pb[s], o[t], 0, 0, 0);
+  };
+  // p of the block in x beside the product of the block in kf, whose logits begin in x
+  auto turn = [&](const Stage<D, NG>* v_of) {
+    f32x16 y;
+    __builtin_amdgcn_sched_barrier(0);
+    if (v_of) load_v(*v_of, 0);
+    product(y);
+    weights(x);
+    __builtin_amdgcn_sched_barrier(0);
+    x = y;
   };
 
   int blk = rg.blk0;
@@ -315,21 +338,46 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
     unpack(lds[0], blk + mine, mine ? pg[1] : pg[0]);
     __syncthreads();
     int buf = 0;
+    if constexpr (AHEAD) {
+      load_k(lds[0], 0);
+      product(x);
+      scale(lds[0], 0);
+      logits(32 * blk, valid(blk, pg[0]));
+    }
     for (;;) {
       const int next = blk + PS;
-      if (next < b1) {
+      const bool rest = next < b1;
+      if (rest) {
 #pragma unroll
         for (int i = 0; i < PS; ++i) more[i] = look_up(next + PS + i);
         fetch(next + mine, mine ? nx[1] : nx[0]);
       }
+      if constexpr (AHEAD) {
+        load_k(lds[buf], 1);
+        turn(&lds[buf]);
+        gather();
+        scale(lds[buf], 1);
+        logits(32 * (blk + 1), valid(blk + 1, pg[1]));
+        load_v(lds[buf], 1);
+      } else {
 #pragma unroll
-      for (int i = 0; i < PS; ++i) {
-        const int t0 = 32 * (blk + i);
-        if (valid(blk + i, pg[i]) && t0 < whi && t0 + 32 > wlo) process(lds[buf], i, t0);
+        for (int i = 0; i < PS; ++i) {
+          const int t0 = 32 * (blk + i);
+          if (!valid(blk + i, pg[i]) || t0 >= whi || t0 + 32 <= wlo) continue;
+          load_k(lds[buf], i);
+          __builtin_amdgcn_sched_barrier(0);
+          product(x);
+          scale(lds[buf], i);
+          load_v(lds[buf], i);
+          __builtin_amdgcn_sched_barrier(0);
+          logits(t0, true);
+          weights(x);
+          gather();
+        }
       }
-      if (next >= b1) break;
+      if (!rest) break;
       unpack(lds[buf ^ 1], next + mine, mine ? nx[1] : nx[0]);
-      __syncthreads();
+      __syncthreads();  // what is still needed of this stage is in registers by now
       buf ^= 1;
       blk = next;
 #pragma unroll
@@ -337,6 +385,17 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
         pg[i] = nx[i];
         nx[i] = more[i];
       }
+      if constexpr (AHEAD) {
+        load_k(lds[buf], 0);
+        turn(nullptr);
+        gather();
+        scale(lds[buf], 0);
+        logits(32 * blk, valid(blk, pg[0]));
+      }
+    }
+    if constexpr (AHEAD) {
+      weights(x);
+      gather();
     }
   }
 

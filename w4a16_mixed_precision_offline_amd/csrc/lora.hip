@@ -53,10 +53,64 @@ __device__ __forceinline__ uint64_t tile_todo(int id, int z) {
   return same != 0 && __builtin_ctzll(same) == z ? same : 0;
 }
 
+// Sums one row's slices of T (columns 8 g .. of every 32) and splits the sum into operands
+// hi and lo, 64 lanes apart for each 32 columns; returns the power of two that they were
+// divided by.
+template <int KR, bool BF>
+__device__ __forceinline__ float split_row(const float* T, size_t step, int slices, size_t row,
+                                           int rank, int g, bool live, u32x4v* hi, u32x4v* lo) {
+  float v[KR][8];
+  float top = 0.f;
+#pragma unroll
+  for (int q = 0; q < KR; ++q) {
+    const int c = 32 * q + 8 * g;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[q][e] = 0.f;
+    if (live && c < rank) {
+      const float* p = T + row + c;
+#pragma unroll 8
+      for (int s = 0; s < slices; ++s) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(p + (size_t)s * step);
+        const f32x4 y = *reinterpret_cast<const f32x4*>(p + (size_t)s * step + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[q][e] += x[e];
+          v[q][4 + e] += y[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[q][e]));
+  }
+  float down = 1.f, up = 1.f;
+  if constexpr (!BF) {
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // 2^-e and 2^e, both normal; an infinite or NaN row keeps its infinities and NaN
+    int ex = (int)(__float_as_uint(top) >> 23) - 127;
+    ex = ex < -100 ? -100 : ex > 100 ? 100 : ex;
+    down = __uint_as_float((uint32_t)(127 - ex) << 23);
+    up = __uint_as_float((uint32_t)(127 + ex) << 23);
+  }
+#pragma unroll
+  for (int q = 0; q < KR; ++q) {
+    float h[8], l[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = v[q][e] * down;
+      h[e] = lo16<BF>(to16<BF>(x));
+      l[e] = fabsf(h[e]) < INFINITY ? x - h[e] : 0.f;
+    }
+    hi[64 * q] = pack8<BF>(h);
+    lo[64 * q] = pack8<BF>(l);
+  }
+  return up;
+}
+
 // T[slice][m][rp] (rp: the rank rounded up to 16) = X[m][its slice of K] A[a]^T.
 // Grid: (slices of K, tiles of 16 TM rows, TM == 1 ? leaders : 1).
 template <int TM, int RT, bool BF>
-__global__ __launch_bounds__(64 * LW) void lora_shrink_kernel(
+__global__ __launch_bounds__(64 * LW, RT * TM <= 16 ? 2 : 1) void lora_shrink_kernel(
     const uint16_t* __restrict__ X, const uint16_t* __restrict__ A, const int* __restrict__ ids,
     float* __restrict__ T, int M, int K, int rank, int adapters, int ldx, int kslice) {
   __shared__ f32x4 red[LW][RT * TM][64];
@@ -82,22 +136,56 @@ __global__ __launch_bounds__(64 * LW) void lora_shrink_kernel(
     // next share cache lines
     const int kw = kslice / LW;
     const int ka = k0 + kw * wave, kb = ka + kw < k1 ? ka + kw : k1;
-#pragma unroll 4
-    for (int kk = ka; kk < kb; kk += 32) {
-      const int k = kk + 8 * g;
+    // rows past A's or X's last repeat it: what comes of them is not stored
+    const uint16_t *ap[RT], *xp[TM];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      ap[i] = Aa + (size_t)(16 * i + r < rank ? 16 * i + r : rank - 1) * K + 8 * g;
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+      xp[t] = X + (size_t)(m0 + 16 * t + r < M ? m0 + 16 * t + r : M - 1) * ldx + 8 * g;
+    // the loads of U steps go out together
+    constexpr int U = RT + TM <= 8 ? 4 : 2;
+    int kk = ka;
+    for (; kk + 32 * U <= kb; kk += 32 * U) {
+      u32x4v af[U][RT], xf[U][TM];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int t = 0; t < TM; ++t) xf[u][t] = *reinterpret_cast<const u32x4v*>(xp[t] + kk + 32 * u);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) af[u][i] = *reinterpret_cast<const u32x4v*>(ap[i] + kk + 32 * u);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int t = 0; t < TM; ++t) acc[i][t] = mfma16<BF>(af[u][i], xf[u][t], acc[i][t]);
+    }
+    for (; kk + 32 <= kb; kk += 32) {
       u32x4v af[RT], xf[TM];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) af[i] = *reinterpret_cast<const u32x4v*>(ap[i] + kk);
+#pragma unroll
+      for (int t = 0; t < TM; ++t) xf[t] = *reinterpret_cast<const u32x4v*>(xp[t] + kk);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int t = 0; t < TM; ++t) acc[i][t] = mfma16<BF>(af[i], xf[t], acc[i][t]);
+    }
+    if (kk < kb) {  // K's last columns; their lanes past the end stay out of both operands
+      u32x4v af[RT], xf[TM];
+      const bool in = kk + 8 * g < kb;
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
         af[i] = u32x4v{0u, 0u, 0u, 0u};
-        if (16 * i + r < rank && k < k1)
-          af[i] = *reinterpret_cast<const u32x4v*>(Aa + (size_t)(16 * i + r) * K + k);
+        if (in) af[i] = *reinterpret_cast<const u32x4v*>(ap[i] + kk);
       }
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
         xf[t] = u32x4v{0u, 0u, 0u, 0u};
-        const int m = m0 + 16 * t + r;
-        if (m < M && k < k1)
-          xf[t] = *reinterpret_cast<const u32x4v*>(X + (size_t)m * ldx + k);
+        if (in) xf[t] = *reinterpret_cast<const u32x4v*>(xp[t] + kk);
       }
 #pragma unroll
       for (int i = 0; i < RT; ++i)
@@ -117,11 +205,29 @@ __global__ __launch_bounds__(64 * LW) void lora_shrink_kernel(
       const int i = p / TM, t = p - i * TM;
       const int mine = __shfl(id, 16 * t + r);
       const int m = m0 + 16 * t + r;
-      if (mine == a && 16 * i < rp)
-        *reinterpret_cast<f32x4*>(T + ((size_t)blockIdx.x * M + m) * rp + 16 * i + 4 * g) = v;
+      if (mine == a && 16 * i < rp) {
+        float* at = T + ((size_t)blockIdx.x * M + m) * rp + 16 * i + 4 * g;
+        *reinterpret_cast<f32x4*>(at) = v;
+      }
     }
     __syncthreads();
   }
+}
+
+// With tiles of many rows the sums are split once, S[tile][hi, lo][row tile][KR][64] and ups[m],
+// for all workgroups that share a tile in the product with B (summed by each of them, 4096
+// rows of rank 64 took 12 us more).  Grid: (row tiles of a tile, tiles), one wave each.
+template <int TM, int KR, bool BF>
+__global__ __launch_bounds__(64) void lora_split_kernel(
+    const float* __restrict__ T, const int* __restrict__ ids, u32x4v* __restrict__ S,
+    float* __restrict__ ups, int M, int rank, int adapters, int slices) {
+  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4, t = blockIdx.x;
+  const int m = blockIdx.y * 16 * TM + 16 * t + r, rp = (rank + 15) & ~15;
+  const int id = m < M ? ids[m] : -1;
+  u32x4v* hi = S + ((size_t)blockIdx.y * 2 * TM + t) * KR * 64 + lane;
+  const float up = split_row<KR, BF>(T, (size_t)M * rp, slices, (size_t)m * rp, rank, g,
+                                     id >= 0 && id < adapters, hi, hi + (size_t)TM * KR * 64);
+  if (g == 0) ups[m] = up;
 }
 
 // Y = base + scale (sum over slices of T) B^T.  A wave takes 64 columns at a time: row i of
@@ -129,9 +235,9 @@ __global__ __launch_bounds__(64 * LW) void lora_shrink_kernel(
 // columns side by side.  Grid: (column pieces, tiles, TM == 1 ? leaders + 1 : 1); the last
 // z of TM == 1 copies the rows without an adapter.
 template <int TM, int KR, bool BF>
-__global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
-    const float* __restrict__ T, const uint16_t* __restrict__ B, const int* __restrict__ ids,
-    const float* __restrict__ scale, const uint16_t* base, uint16_t* Y, int M, int N, int rank,
+__global__ __launch_bounds__(64 * LW, 2) void lora_expand_kernel(
+    const float* __restrict__ T, const u32x4v* __restrict__ S, const float* __restrict__ S_ups,
+    const uint16_t* __restrict__ B, const int* __restrict__ ids, const float* __restrict__ scale, const uint16_t* base, uint16_t* Y, int M, int N, int rank,
     int adapters, int ldy, int slices, int ncols) {
   __shared__ u32x4v split[2][TM][KR][64];  // T's tile as hi and lo operands
   __shared__ float ups[16 * TM];
@@ -162,90 +268,68 @@ __global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
     }
   }
   const int rp = (rank + 15) & ~15;
+  if constexpr (TM > 1) {
+    u32x4v* all = &split[0][0][0][0];
+#pragma unroll
+    for (int i = threadIdx.x; i < 2 * TM * KR * 64; i += 64 * LW)
+      all[i] = S[(size_t)blockIdx.y * (2 * TM * KR * 64) + i];
+    if (threadIdx.x < 16 * TM) ups[threadIdx.x] = S_ups[m0 + threadIdx.x];
+    __syncthreads();
+  }
   while (todo) {
     const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
     todo &= ~__ballot(id == a);
     const uint16_t* Ba = B + (size_t)a * rank * N;
     const float sc = scale[a];
-    // a wave sums one row tile's slices and splits it; all waves take all tiles from LDS
-    for (int t = wave; t < TM; t += LW) {
-      const int m = m0 + 16 * t + r;
-      const bool mine = __shfl(id, 16 * t + r) == a;
-      float v[KR][8];
-      float top = 0.f;
-#pragma unroll
-      for (int q = 0; q < KR; ++q) {
-        const int c = 32 * q + 8 * g;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[q][e] = 0.f;
-        if (mine && c < rank) {
-          const float* p = T + (size_t)m * rp + c;
-#pragma unroll 8
-          for (int s = 0; s < slices; ++s) {
-            const f32x4* at = reinterpret_cast<const f32x4*>(p + (size_t)s * M * rp);
-            const f32x4 x = at[0], y = at[1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[q][e] += x[e];
-              v[q][4 + e] += y[e];
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[q][e]));
-      }
-      float down = 1.f, up = sc;
-      if constexpr (!BF) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        // 2^-e and 2^e, both normal; an infinite or NaN row keeps its infinities and NaN
-        int ex = (int)(__float_as_uint(top) >> 23) - 127;
-        ex = ex < -100 ? -100 : ex > 100 ? 100 : ex;
-        down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        up = sc * __uint_as_float((uint32_t)(127 + ex) << 23);
-      }
-      if (g == 0) ups[16 * t + r] = mine ? up : 0.f;
-#pragma unroll
-      for (int q = 0; q < KR; ++q) {
-        float h[8], l[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = v[q][e] * down;
-          h[e] = lo16<BF>(to16<BF>(x));
-          l[e] = fabsf(h[e]) < INFINITY ? x - h[e] : 0.f;
-        }
-        split[0][t][q][lane] = pack8<BF>(h);
-        split[1][t][q][lane] = pack8<BF>(l);
-      }
-    }
-    __syncthreads();
-    float up[TM];
-    bool mine[TM];
-#pragma unroll
-    for (int t = 0; t < TM; ++t) {
-      up[t] = ups[16 * t + r];
-      mine[t] = __shfl(id, 16 * t + r) == a;
-    }
-    for (int nn = n0; nn < n1; nn += 64 * LW) {
+    // The operands of 64 columns.  Rows of B and of base past the last repeat it: what comes
+    // of them is not stored.
+    struct Columns {
       u32x4v bf[4][KR], b0[TM], b1[TM];
+    };
+    auto load = [&](Columns& c, int nn) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int n = nn + 16 * (r >> 2) + 4 * t + (r & 3);
+        const uint16_t* row = Ba + (size_t)(n < N ? n : N - 1) * rank;
 #pragma unroll
         for (int q = 0; q < KR; ++q) {
-          bf[t][q] = u32x4v{0u, 0u, 0u, 0u};
-          if (n < n1 && 32 * q + 8 * g < rank)
-            bf[t][q] = *reinterpret_cast<const u32x4v*>(Ba + (size_t)n * rank + 32 * q + 8 * g);
+          const int k = 32 * q + 8 * g;
+          c.bf[t][q] = u32x4v{0u, 0u, 0u, 0u};
+          if (k < rank) c.bf[t][q] = *reinterpret_cast<const u32x4v*>(row + k);
         }
       }
       const int n = nn + 16 * g;
 #pragma unroll
       for (int mt = 0; mt < TM; ++mt) {
-        const size_t at = (size_t)(m0 + 16 * mt + r) * ldy + n;
-        b0[mt] = b1[mt] = u32x4v{0u, 0u, 0u, 0u};
-        if (mine[mt] && n < n1) b0[mt] = *reinterpret_cast<const u32x4v*>(base + at);
-        if (mine[mt] && n + 8 < n1) b1[mt] = *reinterpret_cast<const u32x4v*>(base + at + 8);
+        const int m = m0 + 16 * mt + r < M ? m0 + 16 * mt + r : M - 1;
+        const uint16_t* row = base + (size_t)m * ldy;
+        c.b0[mt] = c.b1[mt] = u32x4v{0u, 0u, 0u, 0u};
+        if (TM > 1 || __shfl(id, r) == a) {  // the other leaders' rows are not for this one
+          c.b0[mt] = *reinterpret_cast<const u32x4v*>(row + (n < N ? n : N - 8));
+          c.b1[mt] = *reinterpret_cast<const u32x4v*>(row + (n + 8 < N ? n + 8 : N - 8));
+        }
       }
+    };
+    if constexpr (TM == 1) {
+      if (wave == 0) {
+        const float up = sc * split_row<KR, BF>(
+            T, (size_t)M * rp, slices, (size_t)(m0 + r) * rp, rank, g, __shfl(id, r) == a,
+            &split[0][0][0][lane], &split[1][0][0][lane]);
+        if (g == 0) ups[r] = up;
+      }
+      __syncthreads();
+    }
+    float up[TM];
+    bool mine[TM];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      up[t] = TM == 1 ? ups[r] : sc * ups[16 * t + r];
+      mine[t] = __shfl(id, 16 * t + r) == a;
+    }
+    for (int nn = n0; nn < n1; nn += 64 * LW) {
+      Columns c;
+      load(c, nn);
+      const int n = nn + 16 * g;
 #pragma unroll
       for (int mt = 0; mt < TM; ++mt) {
         const size_t at = (size_t)(m0 + 16 * mt + r) * ldy + n;
@@ -257,16 +341,16 @@ __global__ __launch_bounds__(64 * LW) void lora_expand_kernel(
           const u32x4v hi = split[0][mt][q][lane], lo = split[1][mt][q][lane];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            acc[t] = mfma16<BF>(bf[t][q], lo, acc[t]);
-            acc[t] = mfma16<BF>(bf[t][q], hi, acc[t]);
+            acc[t] = mfma16<BF>(c.bf[t][q], lo, acc[t]);
+            acc[t] = mfma16<BF>(c.bf[t][q], hi, acc[t]);
           }
         }
         float y[8];
-        unpack8<BF>(b0[mt], y);
+        unpack8<BF>(c.b0[mt], y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(up[mt], acc[e >> 2][e & 3], y[e]);
         if (mine[mt] && n < n1) *reinterpret_cast<u32x4v*>(Y + at) = pack8<BF>(y);
-        unpack8<BF>(b1[mt], y);
+        unpack8<BF>(c.b1[mt], y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(up[mt], acc[2 + (e >> 2)][e & 3], y[e]);
         if (mine[mt] && n + 8 < n1) *reinterpret_cast<u32x4v*>(Y + at + 8) = pack8<BF>(y);
@@ -287,12 +371,13 @@ void shrink(dim3 grid, hipStream_t st, const uint16_t* X, const uint16_t* A, con
                      kslice);
 }
 template <int TM, bool BF>
-void expand(dim3 grid, hipStream_t st, const float* T, const uint16_t* B, const int* ids,
+void expand(dim3 grid, hipStream_t st, const float* T, const u32x4v* S, const float* ups,
+            const uint16_t* B, const int* ids,
             const float* scale, const uint16_t* base, uint16_t* Y, int M, int N, int rank,
             int adapters, int ldy, int slices, int ncols) {
   auto fn = rank <= 32 ? lora_expand_kernel<TM, 1, BF>
                        : rank <= 64 ? lora_expand_kernel<TM, 2, BF> : lora_expand_kernel<TM, 4, BF>;
-  hipLaunchKernelGGL(fn, grid, dim3(64 * LW), 0, st, T, B, ids, scale, base, Y, M, N, rank,
+  hipLaunchKernelGGL(fn, grid, dim3(64 * LW), 0, st, T, S, ups, B, ids, scale, base, Y, M, N, rank,
                      adapters, ldy, slices, ncols);
 }
 
@@ -305,15 +390,22 @@ LoraPlan lora_make_plan(int M, int N, int K, int rank) {
   // workgroups: one per (leader, slice); M leaders are the most there can be of few rows
   const int leaders = p.tm == 1 ? M : p.tiles;
   p.kslice = 512;
-  while (p.kslice < K && ((long long)leaders * ((K + p.kslice - 1) / p.kslice) > 512 ||
+  const int most = p.tm == 1 ? 256 : 512;
+  while (p.kslice < K && ((long long)leaders * ((K + p.kslice - 1) / p.kslice) > most ||
                           (K + p.kslice - 1) / p.kslice > 16))
     p.kslice *= 2;
   p.slices = (K + p.kslice - 1) / p.kslice;
   p.ncols = 256;
-  while (p.ncols < 1024 && (long long)p.tiles * ((N + 2 * p.ncols - 1) / (2 * p.ncols)) >= 512)
+  while (p.ncols < 512 && (long long)p.tiles * ((N + 2 * p.ncols - 1) / (2 * p.ncols)) >= 512)
     p.ncols *= 2;
   p.pieces = (N + p.ncols - 1) / p.ncols;
   p.floats = (size_t)p.slices * M * ((rank + 15) / 16 * 16);
+  p.split = 0;
+  if (p.tm > 1) {
+    const int kr = rank <= 32 ? 1 : rank <= 64 ? 2 : 4;
+    p.split = (size_t)p.tiles * 2 * p.tm * kr * 64;  // 16 bytes each
+    p.floats = (p.floats + 3) / 4 * 4 + 4 * p.split + (size_t)p.tiles * 16 * p.tm;
+  }
   return p;
 }
 
@@ -321,6 +413,9 @@ hipError_t lora_launch(const LoraPlan& p, const uint16_t* X, const uint16_t* A, 
                        const int* ids, const float* scale, const uint16_t* base, uint16_t* Y,
                        float* T, int M, int N, int K, int rank, int adapters, int ldx, int ldy,
                        bool bf, hipStream_t st) {
+  const size_t rest = 4 * p.split + (size_t)p.tiles * 16 * p.tm;
+  u32x4v* S = p.tm > 1 ? reinterpret_cast<u32x4v*>(T + (p.floats - rest)) : nullptr;
+  float* ups = p.tm > 1 ? T + (p.floats - (size_t)p.tiles * 16 * p.tm) : nullptr;
   const dim3 g1(p.slices, p.tiles, p.tm == 1 ? 16 : 1);
   const dim3 g2(p.pieces, p.tiles, p.tm == 1 ? 17 : 1);
   if (p.tm == 1) {
@@ -332,12 +427,20 @@ hipError_t lora_launch(const LoraPlan& p, const uint16_t* X, const uint16_t* A, 
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (p.tm > 1) {
+    auto fn = rank <= 32 ? (bf ? lora_split_kernel<4, 1, true> : lora_split_kernel<4, 1, false>)
+              : rank <= 64 ? (bf ? lora_split_kernel<4, 2, true> : lora_split_kernel<4, 2, false>)
+                           : (bf ? lora_split_kernel<4, 4, true> : lora_split_kernel<4, 4, false>);
+    hipLaunchKernelGGL(fn, dim3(4, p.tiles), dim3(64), 0, st, T, ids, S, ups, M, rank, adapters,
+                       p.slices);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   if (p.tm == 1) {
-    (bf ? expand<1, true> : expand<1, false>)(g2, st, T, B, ids, scale, base, Y, M, N, rank,
-                                              adapters, ldy, p.slices, p.ncols);
+    (bf ? expand<1, true> : expand<1, false>)(g2, st, T, S, ups, B, ids, scale, base, Y, M, N,
+                                              rank, adapters, ldy, p.slices, p.ncols);
   } else {
-    (bf ? expand<4, true> : expand<4, false>)(g2, st, T, B, ids, scale, base, Y, M, N, rank,
-                                              adapters, ldy, p.slices, p.ncols);
+    (bf ? expand<4, true> : expand<4, false>)(g2, st, T, S, ups, B, ids, scale, base, Y, M, N,
+                                              rank, adapters, ldy, p.slices, p.ncols);
   }
   return hipGetLastError();
 }
