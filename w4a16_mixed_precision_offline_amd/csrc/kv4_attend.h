@@ -25,16 +25,24 @@ __device__ __forceinline__ half8v codes_subnormal(uint32_t w) {
   return __builtin_bit_cast(half8v, u32x4v{w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu,
                                            v & 0x00F000F0u});
 }
+// (w & mask) | bits in one instruction, which the compiler splits in two; its result goes to
+// vector instructions only
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(w), "s"(mask), "v"(bits));
+  return r;
+}
 // the eight values m + s c of a word; s and m of its tokens in the same order
 __device__ __forceinline__ half8v values(uint32_t w, const u32x4v& s, const u32x4v& m) {
   const uint32_t v = w >> 8;
   const half2v one = {(_Float16)-1024.f, (_Float16)-1024.f};
   const half2v up = {(_Float16)0.0625f, (_Float16)0.0625f};
   const half2v off = {(_Float16)-64.f, (_Float16)-64.f};
-  const half2v c0 = as_half2((w & 0x000F000Fu) | 0x64006400u) + one;
-  const half2v c1 = __builtin_elementwise_fma(as_half2((w & 0x00F000F0u) | 0x64006400u), up, off);
-  const half2v c2 = as_half2((v & 0x000F000Fu) | 0x64006400u) + one;
-  const half2v c3 = __builtin_elementwise_fma(as_half2((v & 0x00F000F0u) | 0x64006400u), up, off);
+  const uint32_t low = 0x000F000Fu, high = 0x00F000F0u, magic = 0x64006400u;
+  const half2v c0 = as_half2(and_or(w, low, magic)) + one;
+  const half2v c1 = __builtin_elementwise_fma(as_half2(and_or(w, high, magic)), up, off);
+  const half2v c2 = as_half2(and_or(v, low, magic)) + one;
+  const half2v c3 = __builtin_elementwise_fma(as_half2(and_or(v, high, magic)), up, off);
   return __builtin_bit_cast(
       half8v, u32x4v{as_word(__builtin_elementwise_fma(c0, as_half2(s[0]), as_half2(m[0]))),
                      as_word(__builtin_elementwise_fma(c1, as_half2(s[1]), as_half2(m[1]))),

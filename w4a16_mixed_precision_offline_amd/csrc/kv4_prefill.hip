@@ -16,9 +16,19 @@
 // into registers before a stage is worked on and unpacked into the other half of LDS after
 // it, with one barrier a stage.
 //
-// p is rounded to fp16 once here, for fp16 rows too: 2^-11 of each p beside 2^-11 of each v.
-// Splitting p as the smaller tiles do would be 8 matrix instructions more on 17, and these
-// bound this kernel together with the exponentials.
+// For fp16 rows p is hi + lo, 22 bits, as with the smaller tiles, at 8 matrix instructions
+// more on 17: with p rounded once the result's error is 1.65 times that of its own rounding,
+// with lo 1.33 times, and 4 sequences of 512 new tokens take 625 us instead of 480.  bf16
+// rows, whose own step is 2^-9, do without.
+//
+// Bound: matrix and vector instructions together.  4 sequences of 4109 to 8192 tokens, 512
+// of them new, 64 query heads on 8 of 128 channels: 370 GFLOP in 625 us, 0.59 PFLOP/s, half
+// of the rate of a large fp16 product (1.2 PFLOP/s), 1060 us with tiles of 16.  Counters (p
+// rounded once): the matrix unit busy 39% and the vector unit 50% of the time, LDS 34%; two
+// waves of 230 registers fit a SIMD and take turns badly.  Measured, not kept: one block's
+// product issued beside the exponentials of the block before it (with p hi + lo 640 us,
+// registers spill), two sums per product instead of one dependent chain (637 us), longest
+// sequences first (no difference).
 #include "kv4_attend.h"
 
 namespace w4a16 {
@@ -185,13 +195,13 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
   auto unpack = [&](Stage<D, NG>& st, int blk, int pg) {
     constexpr int W = D / 32;
     const int t0 = blk * 32, g = lane >> 4, r = lane & 15;
+    if (!valid(blk, pg)) return;  // nobody looks at it
     // what no column sees may be anything: its s and m become 0
-    const bool ok = valid(blk, pg);
-    if (!ok || t0 < rg.lo || t0 + 32 > rg.hi) {
+    if (t0 < rg.lo || t0 + 32 > rg.hi) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int pos = t0 + kv4_slot_token(g, e);
-        if (!ok || pos < rg.lo || pos >= rg.hi) {
+        if (pos < rg.lo || pos >= rg.hi) {
           const uint32_t keep = e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
           for (int i = 0; i < Piece<D, NG>::GH; ++i) {
@@ -223,55 +233,43 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
     }
   };
 
-  constexpr bool AHEAD = NG * D <= 256;  // registers for two blocks at once
-  constexpr int NC = NG, JC = J / NC;
   f32x16 zero;
 #pragma unroll
   for (int i = 0; i < 16; ++i) zero[i] = 0.f;
 
-  // The work on a block is cut where the matrix unit and the vector unit change turns, so
-  // that one block's products run beside another's exponentials:
-  //   load_k, product   x' = m (sum q), acc = c q
-  //   logits            x = x' + s acc, masked; the largest; the reference moved if need be
-  //   weights           p, their sum, p in fp16
-  //   load_v, gather    o += V^T p
-  half8v kf[J], mf, vf[2][CT], pb[2];
-  f32x16 acc[NC], x;
-  auto load_k = [&](const Stage<D, NG>& st, int i_blk) {
-    mf = __builtin_bit_cast(half8v, st.m[i_blk][lane]);
+  auto process = [&](const Stage<D, NG>& st, int i_blk, int t0) {
+    // Both products' operands are read ahead of them, at once: read one by one beside the
+    // matrix instructions they cost 10% more.
+    half8v kf[J], vf[2][CT];
+    const half8v mf = __builtin_bit_cast(half8v, st.m[i_blk][lane]);
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      kf[j] = __builtin_bit_cast(half8v, st.k[i_blk][j / NC + j % NC * JC][lane]);
-  };
-  auto load_v = [&](const Stage<D, NG>& st, int i_blk) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int t = 0; t < CT; ++t) vf[s][t] = __builtin_bit_cast(half8v, st.v[i_blk][s][t][lane]);
-  };
-  auto product = [&](f32x16& y) {
-    y = __builtin_amdgcn_mfma_f32_32x32x16_f16(mf, qm, zero, 0, 0, 0);
+      kf[j] = __builtin_bit_cast(half8v, st.k[i_blk][j / NG + j % NG * JG][lane]);
+    __builtin_amdgcn_sched_barrier(0);
+    f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_f16(mf, qm, zero, 0, 0, 0);
+    f32x16 acc[NG];
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      acc[j % NC] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-          kf[j], qf[j / NC + j % NC * JC], j < NC ? zero : acc[j % NC], 0, 0, 0);
-  };
-  auto scale = [&](const Stage<D, NG>& st, int i_blk) {
+      acc[j % NG] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+          kf[j], qf[j / NG + j % NG * JG], j < NG ? zero : acc[j % NG], 0, 0, 0);
 #pragma unroll
-    for (int q = 0; q < NC; ++q)
+    for (int q = 0; q < NG; ++q)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const f32x4 s = *reinterpret_cast<const f32x4*>(&st.s[i_blk][q][8 * k + 4 * h]);
 #pragma unroll
         for (int i = 4 * k; i < 4 * k + 4; ++i) x[i] = __builtin_fmaf(s[i & 3], acc[q][i], x[i]);
       }
-  };
-  auto logits = [&](int t0, bool ok) {
-    if (!ok || t0 < all_lo || t0 + 32 > all_hi) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < CT; ++t) vf[s][t] = __builtin_bit_cast(half8v, st.v[i_blk][s][t][lane]);
+    __builtin_amdgcn_sched_barrier(0);
+    if (t0 < all_lo || t0 + 32 > all_hi) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int pos = t0 + 4 * h + 8 * (i >> 2) + (i & 3);
-        if (!ok || pos < first || pos > last) x[i] = -INFINITY;
+        if (pos < first || pos > last) x[i] = -INFINITY;
       }
     }
     float top = x[0];
@@ -287,39 +285,39 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
 #pragma unroll
       for (int t = 0; t < CT; ++t) o[t] *= f;
     }
-  };
-  auto weights = [&](const f32x16& y) {
     const float base = kKv4Lift - ref;
     float pr[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      pr[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(y[i], cf, base));
+      pr[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], cf, base));
       sum += pr[i];
     }
+    half8v pb[2], pl[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      pb[s] = __builtin_bit_cast(
-          half8v, u32x4v{pack16<false>(pr[4 * s], pr[4 * s + 1]),
-                         pack16<false>(pr[4 * s + 2], pr[4 * s + 3]),
-                         pack16<false>(pr[4 * s + 8], pr[4 * s + 9]),
-                         pack16<false>(pr[4 * s + 10], pr[4 * s + 11])});
-  };
-  auto gather = [&]() {
+    for (int s = 0; s < 2; ++s) {
+      u32x4v hi, lo;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = pr[4 * s + 8 * (i >> 1) + 2 * (i & 1)];
+        const float b = pr[4 * s + 8 * (i >> 1) + 2 * (i & 1) + 1];
+        hi[i] = pack16<false>(a, b);
+        if constexpr (!BF) lo[i] = pack16<false>(a - lo16<false>(hi[i]), b - hi16<false>(hi[i]));
+      }
+      pb[s] = __builtin_bit_cast(half8v, hi);
+      if constexpr (!BF) pl[s] = __builtin_bit_cast(half8v, lo);
+    }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int t = 0; t < CT; ++t)
         o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[s][t], pb[s], o[t], 0, 0, 0);
-  };
-  // p of the block in x beside the product of the block in kf, whose logits begin in x
-  auto turn = [&](const Stage<D, NG>* v_of) {
-    f32x16 y;
-    __builtin_amdgcn_sched_barrier(0);
-    if (v_of) load_v(*v_of, 0);
-    product(y);
-    weights(x);
-    __builtin_amdgcn_sched_barrier(0);
-    x = y;
+    if constexpr (!BF) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+          o[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[s][t], pl[s], o[t], 0, 0, 0);
+    }
   };
 
   int blk = rg.blk0;
@@ -338,46 +336,21 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
     unpack(lds[0], blk + mine, mine ? pg[1] : pg[0]);
     __syncthreads();
     int buf = 0;
-    if constexpr (AHEAD) {
-      load_k(lds[0], 0);
-      product(x);
-      scale(lds[0], 0);
-      logits(32 * blk, valid(blk, pg[0]));
-    }
     for (;;) {
       const int next = blk + PS;
-      const bool rest = next < b1;
-      if (rest) {
+      if (next < b1) {
 #pragma unroll
         for (int i = 0; i < PS; ++i) more[i] = look_up(next + PS + i);
         fetch(next + mine, mine ? nx[1] : nx[0]);
       }
-      if constexpr (AHEAD) {
-        load_k(lds[buf], 1);
-        turn(&lds[buf]);
-        gather();
-        scale(lds[buf], 1);
-        logits(32 * (blk + 1), valid(blk + 1, pg[1]));
-        load_v(lds[buf], 1);
-      } else {
 #pragma unroll
-        for (int i = 0; i < PS; ++i) {
-          const int t0 = 32 * (blk + i);
-          if (!valid(blk + i, pg[i]) || t0 >= whi || t0 + 32 <= wlo) continue;
-          load_k(lds[buf], i);
-          __builtin_amdgcn_sched_barrier(0);
-          product(x);
-          scale(lds[buf], i);
-          load_v(lds[buf], i);
-          __builtin_amdgcn_sched_barrier(0);
-          logits(t0, true);
-          weights(x);
-          gather();
-        }
+      for (int i = 0; i < PS; ++i) {
+        const int t0 = 32 * (blk + i);
+        if (valid(blk + i, pg[i]) && t0 < whi && t0 + 32 > wlo) process(lds[buf], i, t0);
       }
-      if (!rest) break;
+      if (next >= b1) break;
       unpack(lds[buf ^ 1], next + mine, mine ? nx[1] : nx[0]);
-      __syncthreads();  // what is still needed of this stage is in registers by now
+      __syncthreads();
       buf ^= 1;
       blk = next;
 #pragma unroll
@@ -385,17 +358,6 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
         pg[i] = nx[i];
         nx[i] = more[i];
       }
-      if constexpr (AHEAD) {
-        load_k(lds[buf], 0);
-        turn(nullptr);
-        gather();
-        scale(lds[buf], 0);
-        logits(32 * blk, valid(blk, pg[0]));
-      }
-    }
-    if constexpr (AHEAD) {
-      weights(x);
-      gather();
     }
   }
 
