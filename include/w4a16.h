@@ -440,9 +440,10 @@ size_t w4a16_lora_workspace_bytes(int M, int N, int K, int rank);
  *   lse (device, out) fp32 [tokens][q_heads], may be NULL: the natural logarithm of the sum
  *   of exp(scale * q k).  A token that sees nothing gets out 0 and lse -infinity.  What the
  *   pages hold in places that no token sees does not matter.  max_len: at least the
- *   longest of lens (a longer one is still right, but slow).  The workspace
+ *   longest of lens (a longer one is still right, but slow).  The tokens are divided between
+ *   workgroups by the lengths on the device, the same way every time.  The workspace
  *   (w4a16_kv4_workspace_bytes; 0 for an invalid shape, and where none is needed) is the
- *   stream's, under the rules of w4a16_gemm.
+ *   stream's, under the rules of w4a16_gemm; its arrival counters are left at zero.
  * w4a16_kv4_page_bytes: 0 for an invalid layout. */
 size_t w4a16_kv4_page_bytes(int kv_heads, int head, int group, int page);
 int w4a16_kv4_append(const uint16_t* k, const uint16_t* v, const int32_t* rows,

@@ -15,8 +15,8 @@
 //           by 7, then the sums so far are scaled; p = 2^(x - ref + 8) <= 2^15 is summed in fp32.
 //           For the second product it is rounded to fp16 (2^-11: an eighth of bf16's own
 //           step), and for fp16 rows split into hi + lo, 22 bits, so that V's rounding is the
-//           only one beside that of the result: 1.6 to 1.3 times the error of rounding
-//           alone, at 16 more matrix instructions a block, which a stream from HBM hides.
+//           only one beside that of the result: 1.65 to 1.33 times the error of rounding
+//           alone, at no more (tiles of 8) or 8 more matrix instructions a block.
 //   V^T p^T A = V = m_t + s_t c in fp16 (one rounding of the exact value, 2^-11), B = p, which
 //           is where K q^T left it.  Values past 65504 (a group whose s was rounded up)
 //           saturate (MODE.FP16_OVFL).
@@ -29,6 +29,16 @@
 //
 // The blocks of all tiles are cut into equal stripes, one for each of the workgroups that
 // the card holds at once; the sums of a tile that stripes share are joined in order.
+//
+// Bound: HBM for large caches, latency for small ones.  48 requests to 8192 tokens, 64 query
+// heads on 8 of 128 channels, groups of 64: 234 MB in 48 us, 4.9 TB/s (a large copy: 4.9; 58 us
+// where nothing is left in the 256 MiB cache of an earlier pass); contexts of 131072 and 16538
+// tokens, groups of 32: 189 MB in 50 us (66 us); 3999 tokens of 32 heads: 17 MB in 12.9 us, of
+// which 0.7 us find the part, 1.5 us load q, 2.4 us stream 2 blocks a wave, 1.8 us hand the
+// sums over and 3 us join them.  512 stripes, two to a compute unit, which is what the
+// registers allow: 256 / 768 / 1024 take 59 / 60 / 57 us on the first and 58 / 76 / 87 on the
+// second (50.8 with 512).  Equal stripes without the `lead` of a tile: 75 us on the first.
+// Tiles of 8 columns against 16 where both fit: 49.9 against 56.7 us on the first.
 #include "kv4_attend.h"
 
 namespace w4a16 {
@@ -37,7 +47,11 @@ namespace {
 
 constexpr int AW = 4;              // waves of a workgroup, which share its blocks
 
-constexpr int kPrefillColumns = 64;  // columns of a sequence above which tiles have 128
+// Columns of a sequence above which tiles have 128 (kv4_prefill.hip).  16 against 128, 64 query
+// heads on 8, contexts of 8 x 8192 / 32 x 2048 / 1 x 32768 tokens, us:
+//   32 columns 32 / 32 / 36 against 68 / 65 / 39;   96: 51 / 61 / 53 against 67 / 73 / 47
+//   128: 63 / 71 / 61 against 71 / 73 / 50;         256: 112 / 107 / 104 against 105 / 97 / 76
+constexpr int kPrefillColumns = 128;
 
 // One block of 32 tokens of one kv head in a wave's registers.
 // With tiles of 8 columns a lane needs K's s and m for 4 tokens only (those of tile r / 8).

@@ -23,9 +23,9 @@
 //
 // Bound: matrix and vector instructions together.  4 sequences of 4109 to 8192 tokens, 512
 // of them new, 64 query heads on 8 of 128 channels: 370 GFLOP in 625 us, 0.59 PFLOP/s, half
-// of the rate of a large fp16 product (1.2 PFLOP/s), 1060 us with tiles of 16.  Counters (p
-// rounded once): the matrix unit busy 39% and the vector unit 50% of the time, LDS 34%; two
-// waves of 230 registers fit a SIMD and take turns badly.  Measured, not kept: one block's
+// of the rate of a large fp16 product (1.2 PFLOP/s), 1060 us with tiles of 16.  Counters: the
+// matrix unit busy 47% and the vector unit 52% of the time, LDS 28%; two waves of 210 to 240
+// registers fit a SIMD and take turns badly.  Measured, not kept: one block's
 // product issued beside the exponentials of the block before it (with p hi + lo 640 us,
 // registers spill), two sums per product instead of one dependent chain (637 us), longest
 // sequences first (no difference).

@@ -17,6 +17,12 @@
 // two 16-bit numbers, hi + lo: 22 bits in fp16 (after a power of two per row that puts its
 // largest |T| in [1, 2), so that neither overflow nor underflow touches it), 16 bits in
 // bf16, whose own step is 2^-9.
+//
+// Bound: HBM for many rows, latency for few.  4096 rows, 8192 x 8192, rank 64: 69 us for
+// 201 MB of X, base and Y, 2.9 TB/s (a large copy: 4.9): X A^T 29 us (67 MB, its loads four
+// steps at a time; 37 us one at a time), the split 5 us, T B^T 35 us (134 MB).  48 rows with
+// 40 adapters of rank 16, 8192 x 10240: 14 us; one row, 4096 x 4096: 8.3 us, two launches.
+// Measured, not kept: the slices joined by the last workgroup to arrive (4096 rows 80 us).
 #include "internal.h"
 #include "rows16.h"
 
@@ -385,16 +391,23 @@ void expand(dim3 grid, hipStream_t st, const float* T, const u32x4v* S, const fl
 
 LoraPlan lora_make_plan(int M, int N, int K, int rank) {
   LoraPlan p;
-  p.tm = M > 64 ? 4 : 1;
+  // Tiles of 64 rows share what they read of A and B, tiles of 16 work on an adapter that few of
+  // their rows have with less waste.  8192 x 8192, rank 16, us, 16 against 64: 256 rows of 8
+  // adapters in order 25 / 23, of 32 in any order 37 / 124; 512 rows 26 / 24 and 54 / 130;
+  // 1024 rows 45 / 23 and 103 / 156.
+  p.tm = M > 512 ? 4 : 1;
   p.tiles = (M + 16 * p.tm - 1) / (16 * p.tm);
   // workgroups: one per (leader, slice); M leaders are the most there can be of few rows
   const int leaders = p.tm == 1 ? M : p.tiles;
   p.kslice = 512;
+  // fewer slices leave the second kernel less to add: 48 rows 14.4 us with 256, 15.6 with 512,
+  // 17.2 with 128
   const int most = p.tm == 1 ? 256 : 512;
   while (p.kslice < K && ((long long)leaders * ((K + p.kslice - 1) / p.kslice) > most ||
                           (K + p.kslice - 1) / p.kslice > 16))
     p.kslice *= 2;
   p.slices = (K + p.kslice - 1) / p.kslice;
+  // 4096 rows: 67 us with pieces of 512, 70 with 256 and with 1024
   p.ncols = 256;
   while (p.ncols < 512 && (long long)p.tiles * ((N + 2 * p.ncols - 1) / (2 * p.ncols)) >= 512)
     p.ncols *= 2;

@@ -12,6 +12,9 @@
 // with h scaled by 2^-64, which leaves only true infinities and NaN.  They end as the
 // formula ends: a NaN makes the row's codes NaN, an infinity is a NaN among zeros, and
 // s = 1 for both.
+//
+// Bound: HBM.  8192 x 8192 fp16: 470 MB in 79 us, 5.9 TB/s (a large copy: 4.9); one row of
+// 4096: 2.5 us in the kernel, 5.3 us a call.
 #include "internal.h"
 #include "rows16.h"
 
@@ -164,6 +167,8 @@ hipError_t launch_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* 
                           hipStream_t st) {
   if (M <= 0 || K <= 0 || K % 8 != 0 || K > NORM_MAX_K) return hipErrorInvalidValue;
   const int chunks = K / 8;
+  // 4096 rows of 4096 / 8192 values: 18.7 / 34.8 us with 256 threads, 23.8 / 37.7 with 1024; past
+  // 8192 values 256 threads would need more than 4 chunks each
   const int threads = chunks <= 1024 ? 256 : 1024;
   const int ch = (chunks + threads - 1) / threads;
   NormFn fn = bf ? norm_kernel<true>(threads, ch) : norm_kernel<false>(threads, ch);
