@@ -439,7 +439,8 @@ size_t w4a16_lora_workspace_bytes(int M, int N, int K, int rank);
  *   of q_heads * head, ldq and ldo apart; query head h reads kv head h / (q_heads / kv_heads).
  *   lse (device, out) fp32 [tokens][q_heads], may be NULL: the natural logarithm of the sum
  *   of exp(scale * q k).  A token that sees nothing gets out 0 and lse -infinity.  What the
- *   pages hold in places that no token sees does not matter.  max_len: at least the
+ *   pages hold in places that no token sees does not matter; a NaN reaches every token that
+ *   sees it, and may reach other new tokens of its sequence.  max_len: at least the
  *   longest of lens (a longer one is still right, but slow).  The tokens are divided between
  *   workgroups by the lengths on the device, the same way every time.  The workspace
  *   (w4a16_kv4_workspace_bytes; 0 for an invalid shape, and where none is needed) is the

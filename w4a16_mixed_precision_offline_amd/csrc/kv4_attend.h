@@ -11,11 +11,6 @@ constexpr float kKv4Lazy = 7.f;       // how far a logit may exceed a column's r
 constexpr float kKv4Lift = 8.f;       // p is held times 2^8
 constexpr float kKv4None = -1e30f;    // reference of a column that has seen nothing
 
-// fp16 results past 65504 become 65504 instead of infinity, for the rest of the wave
-__device__ __forceinline__ void saturate_fp16() {
-  __builtin_amdgcn_s_setreg((0 << 11) | (23 << 6) | 1, 1);  // MODE, bit 23, one bit
-}
-
 __device__ __forceinline__ half2v as_half2(uint32_t w) { return __builtin_bit_cast(half2v, w); }
 __device__ __forceinline__ uint32_t as_word(half2v h) { return __builtin_bit_cast(uint32_t, h); }
 
@@ -43,11 +38,16 @@ __device__ __forceinline__ half8v values(uint32_t w, const u32x4v& s, const u32x
   const half2v c1 = __builtin_elementwise_fma(as_half2(and_or(w, high, magic)), up, off);
   const half2v c2 = as_half2(and_or(v, low, magic)) + one;
   const half2v c3 = __builtin_elementwise_fma(as_half2(and_or(v, high, magic)), up, off);
-  return __builtin_bit_cast(
-      half8v, u32x4v{as_word(__builtin_elementwise_fma(c0, as_half2(s[0]), as_half2(m[0]))),
-                     as_word(__builtin_elementwise_fma(c1, as_half2(s[1]), as_half2(m[1]))),
-                     as_word(__builtin_elementwise_fma(c2, as_half2(s[2]), as_half2(m[2]))),
-                     as_word(__builtin_elementwise_fma(c3, as_half2(s[3]), as_half2(m[3])))});
+  // A group whose s was rounded up can pass 65504; NaN stays NaN.  (The saturating mode of
+  // fp16 results would do the first for nothing, but in that mode the matrix instructions
+  // turn a NaN sum into 0.)
+  const half2v most = {(_Float16)65504.f, (_Float16)65504.f};
+  auto value = [&](half2v c, uint32_t sw, uint32_t mw) {
+    return as_word(__builtin_elementwise_minimum(
+        __builtin_elementwise_fma(c, as_half2(sw), as_half2(mw)), most));
+  };
+  return __builtin_bit_cast(half8v, u32x4v{value(c0, s[0], m[0]), value(c1, s[1], m[1]),
+                                           value(c2, s[2], m[2]), value(c3, s[3], m[3])});
 }
 
 // The exponent d by which a query row of largest magnitude `top` is scaled into fp16's top

@@ -19,7 +19,7 @@
 //           alone, at no more (tiles of 8) or 8 more matrix instructions a block.
 //   V^T p^T A = V = m_t + s_t c in fp16 (one rounding of the exact value, 2^-11), B = p, which
 //           is where K q^T left it.  Values past 65504 (a group whose s was rounded up)
-//           saturate (MODE.FP16_OVFL).
+//           become 65504.
 //
 // A token is seen by a column if its position is at most the column's own, more than the
 // column's less the window (window > 0), and its page is in the table.  Blocks that are
@@ -31,7 +31,7 @@
 // the card holds at once; the sums of a tile that stripes share are joined in order.
 //
 // Bound: HBM for large caches, latency for small ones.  48 requests to 8192 tokens, 64 query
-// heads on 8 of 128 channels, groups of 64: 234 MB in 48 us, 4.9 TB/s (a large copy: 4.9; 58 us
+// heads on 8 of 128 channels, groups of 64: 234 MB in 50 us, 4.7 TB/s (a large copy: 4.9; 58 us
 // where nothing is left in the 256 MiB cache of an earlier pass); contexts of 131072 and 16538
 // tokens, groups of 32: 189 MB in 50 us (66 us); 3999 tokens of 32 heads: 17 MB in 12.9 us, of
 // which 0.7 us find the part, 1.5 us load q, 2.4 us stream 2 blocks a wave, 1.8 us hand the
@@ -112,7 +112,6 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
   __shared__ f32x4 red_o[AW][NT][64];
   __shared__ float red_ml[8][8][2];  // [wave][column], or [part][column] of the last join
   __shared__ int arrived;
-  saturate_fp16();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int r = lane & 15, g = lane >> 4;

@@ -88,7 +88,6 @@ template <int D, int NG, bool BF>
 __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
   constexpr int J = D / 16, JG = J / NG, CT = D / 32;
   __shared__ Stage<D, NG> lds[2];
-  saturate_fp16();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int c = lane & 31, h = lane >> 5;
@@ -395,7 +394,6 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
 // the tile's 128 columns, a thread 4 of one.
 template <int D, bool BF>
 __global__ __launch_bounds__(256) void kv4_prefill_join_kernel(Kv4AttendArgs p) {
-  saturate_fp16();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 31, h = lane >> 5, t = blockIdx.y >> 2, k = blockIdx.y & 3;
   const int ratio = p.q_heads / p.heads;
