@@ -1,0 +1,47 @@
+"""What the decoder classes (decoder.py) keep and refuse when the model around them is cast,
+moved, saved or trained: host code only, nothing here reaches a kernel."""
+import pytest
+import torch
+
+from w4a16_mixed_precision_offline_amd.decoder import Adapters
+
+
+def half(*shape):
+    return torch.zeros(shape, dtype=torch.float16)
+
+
+def i32(*shape):
+    return torch.zeros(shape, dtype=torch.int32)
+
+
+def adapters():
+    return Adapters(half(2, 8, 64), half(2, 64, 8), torch.tensor([1 / 3, 3e5]))
+
+
+@pytest.mark.parametrize("cast", [lambda m: m.half(), lambda m: m.bfloat16(), lambda m: m.to(torch.float16), lambda m: m.double(),
+                                  lambda m: torch.nn.ModuleList([m]).half()[0]])
+def test_a_cast_leaves_the_adapters_scale_as_it_is(cast):
+    # the kernel reads it as fp32, and 3e5 has no fp16
+    a = adapters()
+    cast(a)
+    assert a.scale.dtype == torch.float32 and torch.equal(a.scale, torch.tensor([1 / 3, 3e5]))
+
+
+def test_adapters_refuse_weights_of_another_type():
+    x, y, ids = half(3, 64), half(3, 64), i32(3)
+    a = adapters()
+    a.scale = a.scale.half()
+    with pytest.raises(TypeError, match="scale"):
+        a(x, y, ids)
+    a = adapters()
+    a.B = a.B.bfloat16()
+    with pytest.raises(TypeError):
+        a(x, y, ids)
+    a = adapters()
+    a.float()
+    with pytest.raises(TypeError):
+        a(x, y, ids)
+    a = adapters()
+    a.A = half(2, 64, 8).transpose(1, 2)  # the kernel reads [adapters][rank][in]
+    with pytest.raises(ValueError):
+        a(x, y, ids)

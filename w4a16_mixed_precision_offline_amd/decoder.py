@@ -104,7 +104,20 @@ class Adapters(torch.nn.Module):
         for name, x in (("A", A), ("B", B), ("scale", scale)):
             self.register_buffer(name, x.contiguous())
 
+    def _apply(self, fn, recurse=True):
+        # half(), bfloat16() and their like are about A and B: scale stays fp32, bit for bit
+        scale = self.scale
+        super()._apply(fn, recurse)
+        if self.scale.dtype != scale.dtype:
+            self.scale = scale.to(self.scale.device)
+        return self
+
     def forward(self, x: torch.Tensor, y: torch.Tensor, ids: torch.Tensor) -> torch.Tensor:
+        # buffers can have changed since they were checked
+        if self.A.dtype not in _TYPES or self.B.dtype != self.A.dtype or self.scale.dtype != torch.float32:
+            raise TypeError(f"A and B must both be float16 or bfloat16 and scale float32, not {self.A.dtype}, {self.B.dtype} and {self.scale.dtype}")
+        if not (self.A.is_contiguous() and self.B.is_contiguous() and self.scale.is_contiguous()):
+            raise ValueError("A, B and scale must be contiguous")
         adapters, rank, K = self.A.shape
         N = self.B.shape[1]
         ldx, ldy = _rows16("x", x, K), _rows16("y", y, N)
