@@ -3,7 +3,8 @@ moved, saved or trained: host code only, nothing here reaches a kernel."""
 import pytest
 import torch
 
-from w4a16_mixed_precision_offline_amd.decoder import Adapters
+from w4a16_mixed_precision_offline_amd.decoder import Adapters, AttentionBlock, Batch, Kv4Cache
+from w4a16_mixed_precision_offline_amd.layer import W4A16Linear
 
 
 def half(*shape):
@@ -16,6 +17,11 @@ def i32(*shape):
 
 def adapters():
     return Adapters(half(2, 8, 64), half(2, 64, 8), torch.tensor([1 / 3, 3e5]))
+
+
+def block(cache=None):
+    return AttentionBlock(half(256), W4A16Linear(256, 512, device="cpu"), W4A16Linear(256, 256, device="cpu"),
+                          cache or Kv4Cache(4, 2, 64, 64, 32, device="cpu"), 4)
 
 
 @pytest.mark.parametrize("cast", [lambda m: m.half(), lambda m: m.bfloat16(), lambda m: m.to(torch.float16), lambda m: m.double(),
@@ -45,3 +51,11 @@ def test_adapters_refuse_weights_of_another_type():
     a.A = half(2, 64, 8).transpose(1, 2)  # the kernel reads [adapters][rank][in]
     with pytest.raises(ValueError):
         a(x, y, ids)
+
+
+@pytest.mark.parametrize("cast", [torch.bfloat16, torch.float32])
+def test_block_refuses_a_gamma_of_another_type(cast):
+    b = block()
+    b.to(cast)
+    with pytest.raises(TypeError, match="gamma"):
+        b(half(2, 256), None, Batch(i32(3), i32(2), i32(2, 2), 1, 32))

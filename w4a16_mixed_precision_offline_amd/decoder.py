@@ -162,6 +162,8 @@ class AttentionBlock(torch.nn.Module):
             raise ValueError(f"x must be float16 [tokens, {K}]")
         if residual is not None and (residual.dtype != x.dtype or residual.shape != x.shape):
             raise ValueError("residual must be like x")
+        if self.gamma.dtype != x.dtype or not self.gamma.is_contiguous():  # a cast of the model reaches it
+            raise TypeError(f"gamma must be contiguous float16, not {self.gamma.dtype}")
         x = x.contiguous()
         M = x.shape[0]
         h = torch.empty_like(x)
