@@ -59,3 +59,26 @@ def test_block_refuses_a_gamma_of_another_type(cast):
     b.to(cast)
     with pytest.raises(TypeError, match="gamma"):
         b(half(2, 256), None, Batch(i32(3), i32(2), i32(2, 2), 1, 32))
+
+
+def test_host_tensors_are_refused():
+    # their addresses would go to a kernel
+    cache, b = Kv4Cache(4, 2, 64, 64, 32, device="cpu"), Batch(i32(3), i32(2), i32(2, 2), 1, 32)
+    for call in (lambda: cache.append(half(2, 128), half(2, 128), b), lambda: cache.gather(half(2, 128), half(2, 128), b),
+                 lambda: cache.attend(half(2, 256), b, 4), lambda: adapters()(half(3, 64), half(3, 64), i32(3)),
+                 lambda: block()(half(2, 256), None, b)):
+        with pytest.raises(ValueError, match="device"):
+            call()
+
+
+def test_tensors_of_one_call_lie_on_the_current_gpu(monkeypatch):
+    from types import SimpleNamespace
+    from w4a16_mixed_precision_offline_amd import decoder
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    on = [SimpleNamespace(device=torch.device(d)) for d in ("cuda:1", "cuda:1", "cuda:0", "cpu")]
+    decoder._one_gpu(on[0], on[1], None, on[0])
+    for odd in (on[2], on[3]):
+        with pytest.raises(ValueError, match="device"):
+            decoder._one_gpu(odd, on[0])
+        with pytest.raises(ValueError, match="device"):
+            decoder._one_gpu(on[0], None, on[1], odd)

@@ -22,6 +22,16 @@ def _rows16(name: str, x: torch.Tensor, width: int) -> int:
     return x.stride(0) if x.shape[0] > 1 else width
 
 
+def _one_gpu(*tensors: torch.Tensor | None) -> None:
+    """Refuses tensors that are not all on the current GPU: the kernels get bare addresses."""
+    here = tensors[0].device
+    if here.type != "cuda" or here.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors must be on the current GPU, not on device {here}")
+    for x in tensors:
+        if x is not None and x.device != here:
+            raise ValueError(f"the tensors of a call must be on one device, not on {here} and {x.device}")
+
+
 class Batch:
     """The sequences of one step: `rows` int32 [batch + 1] (sequence b's new tokens are rows
     rows[b] .. rows[b + 1] - 1 of q, k and v), `lens` int32 [batch] (lengths with the new
@@ -66,6 +76,7 @@ class Kv4Cache(torch.nn.Module):
         """Quantizes the new tokens' k and v [tokens, kv_heads * head] into their pages."""
         ldk, ldv = self._kv(k, v)
         if k.shape[0] > 0:
+            _one_gpu(self.data, k, v, batch.rows, batch.lens, batch.table)
             w4a16_kv4_append(k, v, batch.rows, batch.lens, batch.table, self.data, batch.size, k.shape[0],
                              min(batch.max_new, k.shape[0]), ldk, ldv, *self._layout(batch), _TYPES[k.dtype])
 
@@ -73,6 +84,7 @@ class Kv4Cache(torch.nn.Module):
         """Writes the cached values of the same tokens to the rows of k and v."""
         ldk, ldv = self._kv(k, v)
         if k.shape[0] > 0:
+            _one_gpu(self.data, k, v, batch.rows, batch.lens, batch.table)
             w4a16_kv4_gather(self.data, batch.rows, batch.lens, batch.table, k, v, batch.size, k.shape[0],
                              min(batch.max_new, k.shape[0]), ldk, ldv, *self._layout(batch), _TYPES[k.dtype])
 
@@ -84,6 +96,7 @@ class Kv4Cache(torch.nn.Module):
             raise ValueError(f"lse must be a contiguous float32 tensor of shape {(q.shape[0], q_heads)}")
         out = torch.empty((q.shape[0], q_heads * self.head), dtype=q.dtype, device=q.device)
         if q.shape[0] > 0:
+            _one_gpu(self.data, q, batch.rows, batch.lens, batch.table, lse)
             w4a16_kv4_attention(q, batch.rows, batch.lens, batch.table, self.data, out, lse, batch.size, q.shape[0],
                                 min(batch.max_new, q.shape[0]), batch.max_len, ldq, q_heads * self.head, q_heads,
                                 *self._layout(batch), window, self.head ** -0.5 if scale is None else scale,
@@ -126,6 +139,7 @@ class Adapters(torch.nn.Module):
         if ids.dtype != torch.int32 or tuple(ids.shape) != (x.shape[0],) or not ids.is_contiguous():
             raise ValueError(f"ids must be a contiguous int32 tensor of {x.shape[0]} values")
         if x.shape[0] > 0:
+            _one_gpu(self.A, self.B, self.scale, x, y, ids)
             w4a16_lora(x, self.A, self.B, ids, self.scale, y, y, x.shape[0], N, K, rank, adapters, ldx, ldy,
                        _TYPES[x.dtype])
         return y
@@ -173,6 +187,7 @@ class AttentionBlock(torch.nn.Module):
         n = torch.empty_like(x) if adapt else None
         if M == 0:
             return torch.empty((0, self.out.out_features), dtype=x.dtype, device=x.device), h
+        _one_gpu(x, residual, self.gamma, self.qkv.wp, self.out.wp)
         w4a8_rmsnorm(x, None if residual is None else residual.contiguous(), self.gamma, h, y8, scale, n, M, K, self.eps, DT_F16)
         qkv = self.qkv(y8, scale)
         if adapt:
