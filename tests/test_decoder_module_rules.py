@@ -82,3 +82,20 @@ def test_tensors_of_one_call_lie_on_the_current_gpu(monkeypatch):
             decoder._one_gpu(odd, on[0])
         with pytest.raises(ValueError, match="device"):
             decoder._one_gpu(on[0], None, on[1], odd)
+
+
+def test_the_cache_is_no_part_of_a_checkpoint():
+    b = block()
+    state = b.state_dict()
+    assert "gamma" in state and not any(n.startswith("cache") for n in state)
+    other = block(Kv4Cache(9, 2, 64, 64, 32, device="cpu"))  # another number of pages
+    other.load_state_dict(state)
+    assert dict(other.named_buffers())["cache.data"].shape[0] == 9
+    # one that was saved with the pages in it loads, and leaves them alone
+    old = {**state, "cache.data": torch.ones(4, 4, dtype=torch.uint8)}
+    before = other.cache.data.clone()
+    other.load_state_dict(old)
+    assert torch.equal(other.cache.data, before)
+    other.cache.load_state_dict({"data": old["cache.data"]})
+    with pytest.raises(RuntimeError):
+        other.load_state_dict({**state, "cache.pages": torch.ones(1)})

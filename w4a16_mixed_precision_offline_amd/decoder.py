@@ -60,7 +60,12 @@ class Kv4Cache(torch.nn.Module):
             raise ValueError(f"unsupported layout: pages={pages}, kv_heads={kv_heads}, head={head} (64 or 128), "
                              f"group={group} (32, 64 or 128, at most head), page={page} (a multiple of 32)")
         self.pages, self.kv_heads, self.head, self.group, self.page = pages, kv_heads, head, group, page
-        self.register_buffer("data", torch.empty((pages, size), dtype=torch.uint8, device=device))
+        # contents of a moment, sized by the machine: moved with the model, but not saved with it
+        self.register_buffer("data", torch.empty((pages, size), dtype=torch.uint8, device=device), persistent=False)
+
+    def _load_from_state_dict(self, state_dict, prefix, *args):
+        state_dict.pop(prefix + "data", None)  # checkpoints that hold the pages of their moment
+        super()._load_from_state_dict(state_dict, prefix, *args)
 
     def _layout(self, batch: Batch):
         return self.kv_heads, self.head, self.group, self.page, self.pages, batch.table.shape[1]
