@@ -99,3 +99,17 @@ def test_the_cache_is_no_part_of_a_checkpoint():
     other.cache.load_state_dict({"data": old["cache.data"]})
     with pytest.raises(RuntimeError):
         other.load_state_dict({**state, "cache.pages": torch.ones(1)})
+
+
+def test_rows_of_no_sequence_attend_to_nothing(monkeypatch):
+    # the kernel leaves them alone: what the caller gets must not be memory of earlier tensors
+    from w4a16_mixed_precision_offline_amd import decoder
+    monkeypatch.setattr(decoder, "_one_gpu", lambda *x: None)
+    monkeypatch.setattr(decoder, "w4a16_kv4_attention", lambda *x: None)
+    torch.use_deterministic_algorithms(True)  # torch.empty gives NaN
+    try:
+        cache = Kv4Cache(4, 2, 64, 64, 32, device="cpu")
+        out = cache.attend(half(5, 256), Batch(i32(3), i32(2), i32(2, 2), 1, 32), 4)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    assert out.shape == (5, 256) and (out == 0).all()

@@ -1,0 +1,45 @@
+"""GPU tests of batches padded to a fixed number of rows, as a captured step has them, through
+the decoder classes."""
+import pytest
+import torch
+
+from test_decoder_block import batch_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("spread", [[(1, 40), (1, 7)], [(70, 70), (9, 33)]])
+def test_rows_of_no_sequence_attend_to_nothing(lib, spread):
+    from w4a16_mixed_precision_offline_amd.decoder import Kv4Cache
+    page, heads, kv, D = 32, 8, 2, 64
+    b = batch_of(spread, page, list(range(16)), "cuda")
+    used = int(b.rows[-1])
+    for shift, pad in ((0, 5), (3, 2)):
+        g = torch.Generator(device="cuda").manual_seed(1)
+        qkv = torch.randn(shift + used + pad, (heads + 2 * kv) * D, generator=g, device="cuda").half()
+        q, k, v = qkv.split([heads * D, kv * D, kv * D], 1)
+        b.rows += shift
+        cache = Kv4Cache(16, kv, D, 32, page)
+        cache.append(k, v, b)
+        torch.use_deterministic_algorithms(True)  # torch.empty gives NaN
+        try:
+            padded = cache.attend(q, b, heads)
+        finally:
+            torch.use_deterministic_algorithms(False)
+        b.rows -= shift
+        alone = cache.attend(q[shift:shift + used], b, heads)
+        assert torch.equal(padded[shift:shift + used], alone) and alone.isfinite().all() and (alone != 0).any(1).all()
+        assert (padded[:shift] == 0).all() and (padded[shift + used:] == 0).all()
+
+
+def test_new_tokens_past_max_new_attend_to_nothing(lib):
+    from w4a16_mixed_precision_offline_amd.decoder import Kv4Cache
+    b = batch_of([(4, 40), (3, 9)], 32, list(range(16)), "cuda")
+    qkv = torch.randn(7, 8 * 64, device="cuda").half()
+    q, k, v = qkv.split([4 * 64, 2 * 64, 2 * 64], 1)
+    cache = Kv4Cache(16, 2, 64, 32, 32)
+    cache.append(k, v, b)
+    full = cache.attend(q, b, 4)
+    b.max_new = 2
+    some = cache.attend(q, b, 4)
+    assert torch.equal(some[[0, 1, 4, 5]], full[[0, 1, 4, 5]]) and (some[[2, 3, 6]] == 0).all()

@@ -95,11 +95,13 @@ class Kv4Cache(torch.nn.Module):
 
     def attend(self, q: torch.Tensor, batch: Batch, q_heads: int, window: int = 0, scale: float | None = None,
                lse: torch.Tensor | None = None) -> torch.Tensor:
-        """Attention of the new tokens q [tokens, q_heads * head] over the cached ones."""
+        """Attention of the new tokens q [tokens, q_heads * head] over the cached ones.  Rows of
+        no sequence (padding, new tokens past batch.max_new) are 0; in lse they keep what they held."""
         ldq = _rows16("q", q, q_heads * self.head)
         if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (q.shape[0], q_heads) or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous float32 tensor of shape {(q.shape[0], q_heads)}")
-        out = torch.empty((q.shape[0], q_heads * self.head), dtype=q.dtype, device=q.device)
+        # which rows have a sequence is known on the device only, and the kernel writes no others
+        out = torch.zeros((q.shape[0], q_heads * self.head), dtype=q.dtype, device=q.device)
         if q.shape[0] > 0:
             _one_gpu(self.data, q, batch.rows, batch.lens, batch.table, lse)
             w4a16_kv4_attention(q, batch.rows, batch.lens, batch.table, self.data, out, lse, batch.size, q.shape[0],
