@@ -113,3 +113,14 @@ def test_rows_of_no_sequence_attend_to_nothing(monkeypatch):
     finally:
         torch.use_deterministic_algorithms(False)
     assert out.shape == (5, 256) and (out == 0).all()
+
+
+def test_adapters_refuse_to_write_behind_autograd():
+    # the kernel writes y in place where no gradient sees it
+    a, y = adapters(), half(3, 64).requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        a(half(3, 64), y, i32(3))
+    with torch.no_grad(), pytest.raises(ValueError, match="device"):  # past that check
+        a(half(3, 64), y, i32(3))
+    with pytest.raises(ValueError, match="device"):  # no gradient reaches x, as with the linear layers
+        a(half(3, 64).requires_grad_(), half(3, 64), i32(3))

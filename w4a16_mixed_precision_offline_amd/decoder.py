@@ -1,7 +1,8 @@
 """The operators of one decoder step over the 4-bit products: a cache of keys and values
 held in 4 bits, and the attention half of a decoder layer that runs norm, products,
 adapters, cache and attention together.  Like the linear layers (layer.py) these classes do
-no arithmetic of their own: they check shapes and forward to the library."""
+no arithmetic of their own: they check shapes and forward to the library.  They are for
+inference: no gradient passes through any of them."""
 from __future__ import annotations
 
 import torch
@@ -145,6 +146,8 @@ class Adapters(torch.nn.Module):
             raise ValueError("x and y must have the same rows and the adapters' type")
         if ids.dtype != torch.int32 or tuple(ids.shape) != (x.shape[0],) or not ids.is_contiguous():
             raise ValueError(f"ids must be a contiguous int32 tensor of {x.shape[0]} values")
+        if y.requires_grad and torch.is_grad_enabled():
+            raise ValueError("y requires a gradient, which would not see what is added in place")
         if x.shape[0] > 0:
             _one_gpu(self.A, self.B, self.scale, x, y, ids)
             w4a16_lora(x, self.A, self.B, ids, self.scale, y, y, x.shape[0], N, K, rank, adapters, ldx, ldy,
