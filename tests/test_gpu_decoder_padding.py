@@ -20,6 +20,7 @@ def test_rows_of_no_sequence_attend_to_nothing(lib, spread):
         q, k, v = qkv.split([heads * D, kv * D, kv * D], 1)
         b.rows += shift
         cache = Kv4Cache(16, kv, D, 32, page)
+        cache.data.zero_()  # the held tokens
         cache.append(k, v, b)
         torch.use_deterministic_algorithms(True)  # torch.empty gives NaN
         try:
@@ -38,6 +39,7 @@ def test_new_tokens_past_max_new_attend_to_nothing(lib):
     qkv = torch.randn(7, 8 * 64, device="cuda").half()
     q, k, v = qkv.split([4 * 64, 2 * 64, 2 * 64], 1)
     cache = Kv4Cache(16, 2, 64, 32, 32)
+    cache.data.zero_()
     cache.append(k, v, b)
     full = cache.attend(q, b, 4)
     b.max_new = 2
