@@ -387,9 +387,11 @@ const char* w4a8_mx_variant_name(int variant);
  *   Y8 (device, out) [M][K] bytes and yscale (device, out) fp32 [M]: X8 and xscale of
  *      w4a8_gemm and w4a8_mx_gemm.  Y8 8-byte aligned.
  *   Y  (device, out) [M][K], y rounded to dtype, may be NULL (w4a16_lora's X, for example).
- * A row of zeros gets yscale 1.  A row with a NaN gets NaN codes, a row with an infinity one
- * NaN per infinity and zeros, yscale 1 both.  Rows of bf16 whose squares pass the fp32 range
- * are normed correctly.  8 <= K <= 65536, K % 8 == 0, eps >= 0. */
+ * yscale is at least 2^-126: where max|y| / 448 is less, the codes are of y / 2^-126.  A row
+ * of zeros gets yscale 1, codes 0 and y 0, whatever eps.  A row with a NaN gets NaN codes, a
+ * row with an infinity one NaN per infinity and zeros, yscale 1 both.  Rows of bf16 whose
+ * squares or products with gamma leave the fp32 range, above or below, are normed correctly.
+ * 8 <= K <= 65536, K % 8 == 0, eps >= 0. */
 int w4a8_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* gamma, uint16_t* H,
                  uint8_t* Y8, float* yscale, uint16_t* Y, int M, int K, float eps, int dtype,
                  void* stream);

@@ -8,10 +8,10 @@
 // y = inv * (h g) with inv > 0 common to the row, so max|y| = inv * max|h g| and
 // y / s = (h g) * (448 / max|h g|), which needs no norm at all.  Sums are fp32.
 //
-// bf16 rows can square past the fp32 range: a row whose sum is not finite is summed again
-// with h scaled by 2^-64, which leaves only true infinities and NaN.  They end as the
-// formula ends: a NaN makes the row's codes NaN, an infinity is a NaN among zeros, and
-// s = 1 for both.
+// bf16 rows can leave the fp32 range, their squares above and below, their products with g
+// too: such rows, and those of zeros, are worked out again in 64 bits, where nothing of
+// theirs can.  True infinities and NaN end as the formula ends: a NaN makes the row's codes
+// NaN, an infinity is a NaN among zeros, and s = 1 for both.
 //
 // Bound: HBM.  8192 x 8192 fp16: 470 MB in 79 us, 5.9 TB/s (a large copy: 4.9); one row of
 // 4096: 2.5 us in the kernel, 5.3 us a call.
@@ -22,8 +22,79 @@ namespace w4a16 {
 
 namespace {
 
-// max|h g| below this is taken as this (448 / max must stay finite)
-constexpr float kTinyTop = 0x1p-110f;
+// Within these bounds fp32 loses nothing that counts: of a mean square above 2^-80, squares
+// below 2^-126 are less than 2^-46; 448 / max|h g| is finite.  yscale is never below 2^-126,
+// where fp32 begins to lose bits.
+constexpr float kLeastMean = 0x1p-80f, kLeastTop = 0x1p-100f, kLeastScale = 0x1p-126f;
+
+// A row that fp32 does not reach, from its beginning, in 64 bits.  It reads the row again
+// (h, where it was written), two values at a time, so that it needs no more registers than
+// the others.
+template <int T, bool BF>
+__device__ __forceinline__ void wide_row(const u32x4v* X, const u32x4v* R, const u32x4v* gamma,
+                                         const u32x4v* H, u32x2v* Y8, float* yscale, u32x4v* Y,
+                                         int K, float eps) {
+  constexpr int NW = T / 64;
+  __shared__ double red[NW][2];
+  const int tid = threadIdx.x, pairs = K / 2;
+  const size_t row = (size_t)blockIdx.x * pairs;
+  const uint32_t* x = reinterpret_cast<const uint32_t*>(H != nullptr ? H : X) + row;
+  const uint32_t* r = H != nullptr || R == nullptr ? nullptr
+                                                   : reinterpret_cast<const uint32_t*>(R) + row;
+  const uint32_t* g = reinterpret_cast<const uint32_t*>(gamma);
+  auto h_pair = [&](int c) {
+    const uint32_t a = x[c];
+    if (r == nullptr) return a;
+    return pack16<BF>(lo16<BF>(a) + lo16<BF>(r[c]), hi16<BF>(a) + hi16<BF>(r[c]));
+  };
+  double ss = 0., top = 0.;
+#pragma unroll 1
+  for (int c = tid; c < pairs; c += T) {
+    const uint32_t h = h_pair(c);
+    const double a = lo16<BF>(h), b = hi16<BF>(h);
+    ss += a * a + b * b;
+    top = fmax(top, fmax(fabs(a * lo16<BF>(g[c])), fabs(b * hi16<BF>(g[c]))));
+  }
+  for (int off = 32; off >= 1; off >>= 1) {
+    ss += __shfl_xor(ss, off);
+    top = fmax(top, __shfl_xor(top, off));
+  }
+  if ((tid & 63) == 0) {
+    red[tid >> 6][0] = ss;
+    red[tid >> 6][1] = top;
+  }
+  __syncthreads();
+  ss = red[0][0];
+  top = red[0][1];
+#pragma unroll 1
+  for (int w = 1; w < NW; ++w) {
+    ss += red[w][0];
+    top = fmax(top, red[w][1]);
+  }
+  const double mean = ss / K + eps;
+  const double inv = mean == 0. ? 0. : 1. / sqrt(mean);  // a row of zeros stays zeros
+  const double exact = inv * top / 448.;
+  float s = 1.f;
+  double up = inv;  // infinite and NaN rows, rows of zeros
+  if (exact > 0. && exact < INFINITY) {
+    s = fmaxf((float)exact, kLeastScale);
+    up = inv / s;
+  } else if (exact == INFINITY) {
+    up = 0.;
+  }
+  if (tid == 0) yscale[blockIdx.x] = s;
+#pragma unroll 1
+  for (int c = tid; c < pairs; c += T) {
+    const uint32_t h = h_pair(c);
+    const double a = lo16<BF>(h), b = hi16<BF>(h), ga = lo16<BF>(g[c]), gb = hi16<BF>(g[c]);
+    const int code =
+        __builtin_amdgcn_cvt_pk_fp8_f32((float)(a * ga * up), (float)(b * gb * up), 0, false);
+    reinterpret_cast<uint16_t*>(Y8)[row + c] = (uint16_t)code;
+    if (Y != nullptr)
+      reinterpret_cast<uint32_t*>(Y)[row + c] =
+          pack16<BF>((float)(a * inv * ga), (float)(b * inv * gb));
+  }
+}
 
 // T threads, CH 16-byte chunks of a row in each.
 template <int T, int CH, bool BF>
@@ -33,7 +104,7 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4
                                                     float* __restrict__ yscale, u32x4v* Y, int K,
                                                     float eps) {
   constexpr int NW = T / 64;
-  __shared__ float red[2][NW][2];
+  __shared__ float red[NW][2];
   const int tid = threadIdx.x;
   const int chunks = K / 8;
   const size_t row = (size_t)blockIdx.x * chunks;
@@ -72,8 +143,8 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4
       if (c < chunks) H[row + c] = h[j];
     }
   }
-  // the row's sum of squares and largest |h g|, with h times `pre`
-  auto reduce = [&](float pre, int slot, float& ss, float& top) {
+  // the row's sum of squares and largest |h g|
+  auto reduce = [&](float& ss, float& top) {
     ss = 0.f;
     top = 0.f;
 #pragma unroll
@@ -83,9 +154,8 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4
       unpack8<BF>(gm[j], g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float v = a[e] * pre;
-        ss = __builtin_fmaf(v, v, ss);
-        top = fmaxf(top, fabsf(v * g[e]));
+        ss = __builtin_fmaf(a[e], a[e], ss);
+        top = fmaxf(top, fabsf(a[e] * g[e]));
       }
     }
 #pragma unroll
@@ -95,46 +165,44 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4
     }
     if constexpr (NW > 1) {
       if ((tid & 63) == 0) {
-        red[slot][tid >> 6][0] = ss;
-        red[slot][tid >> 6][1] = top;
+        red[tid >> 6][0] = ss;
+        red[tid >> 6][1] = top;
       }
       __syncthreads();
-      ss = red[slot][0][0];
-      top = red[slot][0][1];
+      ss = red[0][0];
+      top = red[0][1];
 #pragma unroll
       for (int w = 1; w < NW; ++w) {
-        ss += red[slot][w][0];
-        top = fmaxf(top, red[slot][w][1]);
+        ss += red[w][0];
+        top = fmaxf(top, red[w][1]);
       }
     }
   };
-  float ss, top, pre = 1.f;
-  reduce(1.f, 0, ss, top);
-  float inv = rsqrtf(ss / (float)K + eps);
-  if (!(ss < INFINITY)) {  // the same for the whole workgroup
-    pre = 0x1p-64f;
-    reduce(pre, 1, ss, top);
-    inv = rsqrtf(ss / (float)K);  // eps * 2^-128 is nothing beside it
+  float ss, top;
+  reduce(ss, top);
+  const float mean = ss / (float)K + eps;
+  const float inv = rsqrtf(mean);
+  const float s = inv * top * (1.f / 448.f);
+  // the same for the whole workgroup (the ballot shows it to the compiler)
+  const bool narrow = ss < INFINITY && mean >= kLeastMean && top >= kLeastTop &&
+                      s >= kLeastScale && s < INFINITY;
+  if (__ballot(!narrow) != 0) {
+    wide_row<T, BF>(X, R, gamma, H, Y8, yscale, Y, K, eps);
+    return;
   }
-  const bool zero = top == 0.f;
-  top = fmaxf(top, kTinyTop);
-  float up = 448.f / top;
-  float s = inv * top * (1.f / 448.f);
-  if (ss != ss) up = NAN;
-  if (zero || !(s > 0.f && s < INFINITY)) s = 1.f;
+  const float up = 448.f / top;
   if (tid == 0) yscale[blockIdx.x] = s;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int c = tid + j * T;
     if (c >= chunks) continue;
+    // unpacked again: the compiler would hold all of h g since the sums, twice the registers
+    asm("" : "+v"(h[j]));
     float a[8], g[8], y[8];
     unpack8<BF>(h[j], a);
     unpack8<BF>(gm[j], g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] *= pre;
-      y[e] = a[e] * g[e] * up;
-    }
+    for (int e = 0; e < 8; ++e) y[e] = a[e] * g[e] * up;
     int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
     int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
