@@ -38,6 +38,10 @@ namespace {
 constexpr int PTC = 128;  // columns of a workgroup
 constexpr int PS = 2;     // blocks of a stage
 
+// p's exponent is x cf - ref + 8 in one fma.  ref is some x cf rounded, so past 2^26 their
+// difference alone can lift p out of fp16: past this reference x cf is rounded first.
+constexpr float kFar = 0x1p20f;
+
 template <int D, int NG>
 struct Stage {
   u32x4v k[PS][D / 16][64];
@@ -171,6 +175,7 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
   float ref = kKv4None, sum = 0.f;
+  bool far = false;  // of the whole wave: some column's reference is past kFar
 
   const int page_blocks = p.page / 32;
   const size_t page_bytes = (size_t)p.heads * page_blocks * kv4_block_bytes(D, NG);
@@ -275,7 +280,9 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, x[i]);
     top *= cf;
-    if (__ballot(top > ref + kKv4Lazy) != 0) {
+    float by = cf;
+    if (__ballot(top > ref + kKv4Lazy) != 0 || far) {
+#pragma clang fp contract(off)
       top = fmaxf(top, __shfl_xor(top, 32));
       const float next = fmaxf(ref, top);
       const float f = __builtin_amdgcn_exp2f(ref - next);
@@ -283,12 +290,18 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
       sum *= f;
 #pragma unroll
       for (int t = 0; t < CT; ++t) o[t] *= f;
+      far = __ballot(ref != kKv4None && fabsf(ref) > kFar) != 0;
+      if (far) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * cf - ref;
+        by = 1.f;
+      }
     }
-    const float base = kKv4Lift - ref;
+    const float base = far ? kKv4Lift : kKv4Lift - ref;
     float pr[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      pr[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], cf, base));
+      pr[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], by, base));
       sum += pr[i];
     }
     half8v pb[2], pl[2];
