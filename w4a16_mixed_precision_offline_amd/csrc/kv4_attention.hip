@@ -203,7 +203,7 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
 
   // q, scaled, and its sums per group of channels (times 2^-24, the codes' unit)
   half8v qf[TC == 8 ? 2 : 1][J];
-  float qsum[NG], cf;
+  float qsum[NG], cf, more;
   {
     float f[J][8], top = 0.f;
 #pragma unroll
@@ -244,8 +244,12 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
       qsum[q] += __shfl_xor(qsum[q], 32);
       qsum[q] *= 0x1p-24f;
     }
-    cf = __builtin_ldexpf(p.scale * 1.4426950408889634f, 24 - d);
+    // bf16 queries past 2^91 need more than fp32 has in one factor
+    const int over = BF && d < -76 ? -76 - d : 0;
+    cf = __builtin_ldexpf(p.scale * 1.4426950408889634f, 24 - d - over);
+    more = __builtin_ldexpf(1.f, over);
   }
+  const bool big = BF && __ballot(more != 1.f) != 0;
 
   f32x4 o[NT];
 #pragma unroll
@@ -280,6 +284,10 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
       }
 #pragma unroll
     for (int e = 0; e < E; ++e) x[e] *= cf;
+    if (big) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] *= more;
+    }
     if (t0 < all_lo || t0 + 32 > all_hi) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
