@@ -57,3 +57,10 @@ def test_large_logits(lib, tile, D, G, t, q, k):
 @pytest.mark.parametrize("q,k", [(6e36, 1.0), (1.2e37, 0.5), (3e38, 1e-3)])
 def test_bf16_queries_near_the_end_of_their_range(lib, tile, D, G, q, k):
     one_hot(lib, tile, BF16, D, G, q, k)
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("D,G", [(64, 64), (128, 32)])
+@pytest.mark.parametrize("q,k", [(-6e36, 1.0), (-1e32, 1.0), (-1e30, 1.0), (1e28, -1e3)])
+def test_logits_far_below_zero(lib, tile, D, G, q, k):
+    one_hot(lib, tile, BF16, D, G, q, k)

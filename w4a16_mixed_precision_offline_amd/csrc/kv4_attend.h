@@ -9,7 +9,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kKv4Lazy = 7.f;       // how far a logit may exceed a column's reference
 constexpr float kKv4Lift = 8.f;       // p is held times 2^8
-constexpr float kKv4None = -1e30f;    // reference of a column that has seen nothing
+// Reference of a column that has seen nothing, the lowest number: no finite logit is below it.
+constexpr float kKv4None = -0x1.fffffep127f;
 
 __device__ __forceinline__ half2v as_half2(uint32_t w) { return __builtin_bit_cast(half2v, w); }
 __device__ __forceinline__ uint32_t as_word(half2v h) { return __builtin_bit_cast(uint32_t, h); }
