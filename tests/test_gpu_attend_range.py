@@ -64,3 +64,17 @@ def test_bf16_queries_near_the_end_of_their_range(lib, tile, D, G, q, k):
 @pytest.mark.parametrize("q,k", [(-6e36, 1.0), (-1e32, 1.0), (-1e30, 1.0), (1e28, -1e3)])
 def test_logits_far_below_zero(lib, tile, D, G, q, k):
     one_hot(lib, tile, BF16, D, G, q, k)
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("t,q,scale", [(BF16, 1e-37, 1e-25), (BF16, 1e-30, 1e-38), (F16, 1e-6, 1e-38), (F16, 1.0, 1e-38)])
+def test_scales_that_leave_nothing_of_the_logits(lib, tile, t, q, scale):
+    n0, n1 = TILES[tile]
+    s = Setup([(n0, 200), (n1, 90)], 1, 64, 64, 64, t, q_heads=2)
+    s.qkv[:, :128] = (s.qkv[:, :128].float() * q).to(t)
+    s.fill()
+    s.append_model()
+    s.device()
+    for window in (0, 40):
+        out, lse = s.attend(lib, window, scale)
+        s.check_attend(out, lse, window, scale, rows=[0, 1, 7, 31, 33, 69])

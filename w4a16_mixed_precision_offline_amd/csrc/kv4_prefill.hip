@@ -166,7 +166,8 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
       }
     }
     qm = __builtin_bit_cast(half8v, pack8<false>(x));
-    cf = __builtin_ldexpf(p.scale * 1.4426950408889634f, 8 - d);
+    // above 0, which would make NaN of a masked logit; what is less leaves nothing of the others
+    cf = fmaxf(__builtin_ldexpf(p.scale * 1.4426950408889634f, 8 - d), 0x1p-126f);
   }
 
   f32x16 o[CT];
