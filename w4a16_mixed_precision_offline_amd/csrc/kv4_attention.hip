@@ -324,6 +324,7 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
     float pr[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+#pragma clang fp contract(off)  // ref is some x cf rounded: so has to be each that it is taken from
       pr[e] = __builtin_amdgcn_exp2f(x[e] - ref + kKv4Lift);
       sum += pr[e];
     }
