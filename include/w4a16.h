@@ -406,7 +406,10 @@ int w4a8_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* gamma, ui
  * An id below 0 or >= adapters means no adapter: Y[m] = base[m].  Any order of ids is
  * right; rows of one adapter side by side are fastest.  K % 8 == 0, N % 8 == 0,
  * rank % 8 == 0, rank <= 128, M <= 2^21.  The workspace (w4a16_lora_workspace_bytes; 0 for
- * an invalid shape) is the stream's, under the rules of w4a16_gemm. */
+ * an invalid shape) is the stream's, under the rules of w4a16_gemm.  One call with the most
+ * rows and the highest rank before a capture covers the others: a buffer of the library's own
+ * is made large enough for them.  One of the caller's has to hold what the query says of each
+ * shape: fewer rows can need more, since they are cut into more slices. */
 int w4a16_lora(const uint16_t* X, const uint16_t* A, const uint16_t* B, const int32_t* ids,
                const float* scale, const uint16_t* base, uint16_t* Y, int M, int N, int K, int rank,
                int adapters, int ldx, int ldy, int dtype, void* stream);
@@ -446,7 +449,10 @@ size_t w4a16_lora_workspace_bytes(int M, int N, int K, int rank);
  *   longest of lens (a longer one is still right, but slow).  The tokens are divided between
  *   workgroups by the lengths on the device, the same way every time.  The workspace
  *   (w4a16_kv4_workspace_bytes; 0 for an invalid shape, and where none is needed) is the
- *   stream's, under the rules of w4a16_gemm; its arrival counters are left at zero.
+ *   stream's, under the rules of w4a16_gemm; its arrival counters are left at zero.  As with
+ *   w4a16_lora one call before a capture covers the smaller ones, here all of the same head
+ *   whose max_new * q_heads / kv_heads is no larger (or both above 128), and a buffer of the
+ *   caller's has to hold each shape's own: a few tokens can need more than many.
  * w4a16_kv4_page_bytes: 0 for an invalid layout. */
 size_t w4a16_kv4_page_bytes(int kv_heads, int head, int group, int page);
 int w4a16_kv4_append(const uint16_t* k, const uint16_t* v, const int32_t* rows,

@@ -81,21 +81,22 @@ bool capturing(hipStream_t st) {
   return cs != hipStreamCaptureStatusNone;
 }
 
+// `most_*`: what the largest smaller shape could need, where plans are not monotone.  A buffer
+// of the library's own is made that large whenever it may be, so that a later capture of a
+// smaller shape finds room.
 int get_workspace(int dev, hipStream_t st, size_t counters, size_t floats, int** cnt,
-                  float** part) {
+                  float** part, size_t most_counters = 0, size_t most_floats = 0) {
   *cnt = nullptr;
   *part = nullptr;
-  if (counters == 0 && floats == 0) return W4A16_OK;
+  if (most_counters < counters) most_counters = counters;
+  if (most_floats < floats) most_floats = floats;
+  if (most_counters == 0 && most_floats == 0) return W4A16_OK;
   std::lock_guard<std::mutex> lk(g_mu);
   Workspace& ws = g_ws[std::make_pair(dev, st)];
-  if (ws.external) {
-    if (ws.counter_ints < counters || ws.part_floats < floats) return W4A16_ERR_WORKSPACE;
-  } else if (ws.ptr == nullptr || ws.counter_ints < counters || ws.part_floats < floats) {
-    // a graph being captured cannot take the allocation and the clearing of the counters:
-    // the first call of a shape on a stream must come before any capture on it
-    if (capturing(st)) return W4A16_ERR_WORKSPACE;
-    size_t c = counters > ws.counter_ints ? counters : ws.counter_ints;
-    size_t f = floats > ws.part_floats ? floats : ws.part_floats;
+  auto holds = [&](size_t c, size_t f) { return ws.counter_ints >= c && ws.part_floats >= f; };
+  auto grow = [&](size_t c, size_t f) {
+    if (c < ws.counter_ints) c = ws.counter_ints;
+    if (f < ws.part_floats) f = ws.part_floats;
     if (ws.ptr) {
       if (c > ws.counter_ints && c < 2 * ws.counter_ints) c = 2 * ws.counter_ints;
       if (f > ws.part_floats && f < 2 * ws.part_floats) f = 2 * ws.part_floats;
@@ -104,17 +105,30 @@ int get_workspace(int dev, hipStream_t st, size_t counters, size_t floats, int**
     void* p = nullptr;
     if (hipMalloc(&p, c * sizeof(int) + f * sizeof(float)) != hipSuccess) {
       (void)hipGetLastError();
-      return W4A16_ERR_WORKSPACE;
+      return false;
     }
     if (hipMemsetAsync(p, 0, c * sizeof(int), st) != hipSuccess) {
       (void)hipGetLastError();
       (void)hipFree(p);
-      return W4A16_ERR_WORKSPACE;
+      return false;
     }
     if (ws.ptr) g_retired.push_back(ws.ptr);
     ws.ptr = p;
     ws.counter_ints = c;
     ws.part_floats = f;
+    return true;
+  };
+  if (ws.external) {
+    if (!holds(counters, floats)) return W4A16_ERR_WORKSPACE;
+  } else if (!holds(most_counters, most_floats)) {
+    // a graph being captured cannot take the allocation and the clearing of the counters:
+    // the first call of a shape on a stream must come before any capture on it
+    if (capturing(st)) {
+      if (!holds(counters, floats)) return W4A16_ERR_WORKSPACE;
+    } else if (!grow(most_counters, most_floats) && !holds(counters, floats) &&
+               !grow(counters, floats)) {
+      return W4A16_ERR_WORKSPACE;
+    }
   }
   *cnt = static_cast<int*>(ws.ptr);
   *part = reinterpret_cast<float*>(static_cast<int*>(ws.ptr) + ws.counter_ints);
@@ -885,7 +899,8 @@ int w4a16_lora(const uint16_t* X, const uint16_t* A, const uint16_t* B, const in
   const LoraPlan plan = lora_make_plan(M, N, K, rank);
   int* cnt;
   float* part;
-  if ((rc = get_workspace(dev, st, 0, plan.floats, &cnt, &part))) return rc;
+  if ((rc = get_workspace(dev, st, 0, plan.floats, &cnt, &part, 0, lora_most_floats(M, rank))))
+    return rc;
   return launched(lora_launch(plan, X, A, B, ids, scale, base, Y, part, M, N, K, rank, adapters,
                               ldx, ldy, dtype == W4A16_DT_BF16, st));
 }
@@ -983,7 +998,9 @@ int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* l
       kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
   int* cnt;
   float* part;
-  if ((rc = get_workspace(dev, st, plan.counters, plan.floats, &cnt, &part))) return rc;
+  if ((rc = get_workspace(dev, st, plan.counters, plan.floats, &cnt, &part, KV4_STRIPES,
+                          kv4_attend_most_floats(plan.cols, head))))
+    return rc;
   Kv4AttendArgs a{};
   a.q = q;
   a.rows = rows;

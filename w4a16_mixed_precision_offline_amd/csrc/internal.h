@@ -188,6 +188,7 @@ struct LoraPlan {
   size_t split;             // operands of the split sums
 };
 LoraPlan lora_make_plan(int M, int N, int K, int rank);
+size_t lora_most_floats(int M, int rank);  // of any plan of at most M rows and that rank
 hipError_t lora_launch(const LoraPlan& p, const uint16_t* X, const uint16_t* A, const uint16_t* B,
                        const int* ids, const float* scale, const uint16_t* base, uint16_t* Y,
                        float* T, int M, int N, int K, int rank, int adapters, int ldx, int ldy,
@@ -216,7 +217,7 @@ struct Kv4AttendArgs {
   uint16_t* out;
   float* lse;     // may be NULL
   float *part_o, *part_ml;
-  int* counters;  // zero at rest, one per tile
+  int* counters;  // zero at rest, one per stripe
   int batch, tokens, max_new, ldq, ldo, q_heads, heads, page, pages, width, window;
   float scale;
   int col_tiles;      // tiles of query columns per sequence and kv head
@@ -229,6 +230,9 @@ struct Kv4AttendPlan {
   int col_tiles, target, chunk, chunks, slots, tiles;  // as in Kv4AttendArgs; slots 0: no chunks
   size_t floats, counters;  // workspace
 };
+constexpr int KV4_STRIPES = 512;  // most stripes of a launch, and the wide tiles' target
+// workspace of any plan whose tiles have at most that many columns
+size_t kv4_attend_most_floats(int cols, int D);
 Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, int q_heads,
                               int heads, int D, int window);
 hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& a, int D, int groups,

@@ -546,6 +546,11 @@ AttendFn attend_kernel(int D, int groups) {
 
 }  // namespace
 
+size_t kv4_attend_most_floats(int cols, int D) {
+  // two slots a stripe of narrow tiles; fewer than target + target chunks of wide ones
+  return (size_t)2 * KV4_STRIPES * cols * (D + 2);
+}
+
 Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, int q_heads,
                               int heads, int D, int window) {
   Kv4AttendPlan p{};
@@ -562,7 +567,7 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
   if (window > 0 && span > ((long long)window + p.cols / ratio + 1) / 32 + 2)
     span = ((long long)window + p.cols / ratio + 1) / 32 + 2;
   if (p.cols == 128) {
-    p.target = 512;
+    p.target = KV4_STRIPES;
     p.chunk = 16;
     p.chunks = (int)((span + p.chunk - 1) / p.chunk);
     if (p.chunks <= 1 || tiles >= p.target || batch > 1024) {
@@ -577,7 +582,7 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     p.chunk = 8;
     long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
     if (batch > 1024 || stripes <= tiles) return p;
-    if (stripes > 512) stripes = 512;
+    if (stripes > KV4_STRIPES) stripes = KV4_STRIPES;
     p.target = (int)stripes;
     p.slots = 2 * (int)stripes;
     p.counters = (size_t)stripes;

@@ -389,6 +389,21 @@ void expand(dim3 grid, hipStream_t st, const float* T, const u32x4v* S, const fl
 
 }  // namespace
 
+namespace {
+// workspace of the split sums and their powers of two (tiles of 64 rows)
+size_t split_floats(int tiles, int tm, int rank) {
+  const int kr = rank <= 32 ? 1 : rank <= 64 ? 2 : 4;
+  return (size_t)tiles * (4 * 2 * tm * kr * 64 + 16 * tm);
+}
+}  // namespace
+
+size_t lora_most_floats(int M, int rank) {
+  // rows times slices: at most 256 or M in tiles of 16, 64 * 512 or M in tiles of 64
+  const size_t rp = (rank + 15) / 16 * 16;
+  if (M <= 512) return (M < 256 ? 256 : M) * rp;
+  return (M < 32768 ? 32768 : M) * rp + split_floats((M + 63) / 64, 4, rank);
+}
+
 LoraPlan lora_make_plan(int M, int N, int K, int rank) {
   LoraPlan p;
   // Tiles of 64 rows share what they read of A and B, tiles of 16 work on an adapter that few of
@@ -417,7 +432,7 @@ LoraPlan lora_make_plan(int M, int N, int K, int rank) {
   if (p.tm > 1) {
     const int kr = rank <= 32 ? 1 : rank <= 64 ? 2 : 4;
     p.split = (size_t)p.tiles * 2 * p.tm * kr * 64;  // 16 bytes each
-    p.floats = (p.floats + 3) / 4 * 4 + 4 * p.split + (size_t)p.tiles * 16 * p.tm;
+    p.floats += split_floats(p.tiles, p.tm, rank);
   }
   return p;
 }
