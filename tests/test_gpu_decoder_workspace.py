@@ -90,3 +90,43 @@ def test_one_call_covers_the_attention_of_fewer_tokens(lib, batch, new, max_len)
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(a.out[:s[0] * s[1]], want[:s[0] * s[1]]), s
+
+
+def test_buffers_of_the_callers(lib):
+    a, side = Arena(2048), torch.cuda.Stream()
+    # (what to run, its workspace): adapters in both tiles, attention in tiles of 8, 16 and 128 columns
+    lora = [(m, 1024, 1024, r) for m, r in ((16, 64), (700, 64))]
+    attend = [(1, 1, 4096), (2, 9, 4096), (1, 300, 4096)]
+    todo = [(lib.w4a16_lora_workspace_bytes(*s), lambda st=None, s=s: a.lora(lib, *s, st), a.y) for s in lora]
+    for s in attend:
+        need = lib.w4a16_kv4_workspace_bytes(s[0], s[0] * s[1], s[1], s[2], HEADS, KV, D)
+        todo.append((need, lambda st=None, s=s, rows=a.rows(s[0], s[1]): a.attend(lib, rows, *s, st), a.out))
+    for need, call, out in todo:
+        assert need > 0
+        out.zero_()
+        call()
+        torch.cuda.synchronize()
+        want = out.clone()
+        room = lib.WS_COUNTER_BYTES + need
+        buf = torch.zeros(room + 4096, dtype=torch.uint8, device="cuda")
+        buf[room:] = 77
+        torch.cuda.synchronize()
+        lib.w4a16_set_workspace(buf, room, stream=side)
+        try:
+            for _ in range(2):  # the counters are left at zero
+                out.zero_()
+                torch.cuda.synchronize()
+                call(side)
+                side.synchronize()
+                assert torch.equal(out, want)
+            assert (buf[:lib.WS_COUNTER_BYTES] == 0).all() and (buf[room:] == 77).all()
+            lib.w4a16_set_workspace(buf, lib.WS_COUNTER_BYTES + need // 4, stream=side)
+            out.fill_(5.0)
+            torch.cuda.synchronize()
+            with pytest.raises(lib.W4A16Error) as e:
+                call(side)
+            assert e.value.code == -6
+            side.synchronize()
+            assert (out == 5.0).all()  # nothing was launched
+        finally:
+            lib.w4a16_set_workspace(None, 0, stream=side)
