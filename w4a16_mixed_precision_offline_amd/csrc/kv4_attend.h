@@ -81,14 +81,22 @@ __device__ __forceinline__ int kv4_span(const Kv4AttendArgs& p, const Kv4Seq& s,
   return span < 1 ? 1 : span;
 }
 
+// A launch without chunks can have more workgroups than one dimension of a grid takes (2^32
+// threads: 1024 sequences of 8 kv heads of which one brings 32768 tokens): rows of 2^20.
+constexpr unsigned kKv4GridRow = 1u << 20;
+inline dim3 kv4_grid(unsigned n) {
+  return n <= kKv4GridRow ? dim3(n) : dim3(kKv4GridRow, (n + kKv4GridRow - 1) / kKv4GridRow);
+}
+
 // Where a launch without chunks starts: workgroups go round robin to the 8 XCDs, each with
 // an L2 of its own, so that the tiles of one (sequence, kv head) take one residue of 8 and
 // share the cached bytes.
 __device__ __forceinline__ bool kv4_place_whole(const Kv4AttendArgs& p, Kv4Place& w) {
-  const unsigned unit = blockIdx.x % 8 + 8 * (blockIdx.x / 8 / p.col_tiles);
+  const unsigned id = blockIdx.x + blockIdx.y * kKv4GridRow;
+  const unsigned unit = id % 8 + 8 * (id / 8 / p.col_tiles);
   if (unit >= (unsigned)p.heads * p.batch) return false;
   // the last tiles see the most: they start first
-  w.tile = p.col_tiles - 1 - (int)(blockIdx.x / 8 % p.col_tiles);
+  w.tile = p.col_tiles - 1 - (int)(id / 8 % p.col_tiles);
   w.head = unit % p.heads;
   w.b = unit / p.heads;
   w.s = kv4_seq(p.rows, p.lens, w.b, p.tokens, p.max_new);

@@ -607,7 +607,7 @@ hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& arg
                           ? (bf ? attend_kernel<8, true>(D, groups) : attend_kernel<8, false>(D, groups))
                           : (bf ? attend_kernel<16, true>(D, groups)
                                 : attend_kernel<16, false>(D, groups));
-  hipLaunchKernelGGL(fn, dim3(grid), dim3(64 * AW), 0, st, a);
+  hipLaunchKernelGGL(fn, kv4_grid(grid), dim3(64 * AW), 0, st, a);
   return hipGetLastError();
 }
 

@@ -453,7 +453,7 @@ hipError_t launch_kv4_prefill(const Kv4AttendArgs& a, int D, int groups, bool bf
   const long long units = ((long long)a.heads * a.batch + 7) / 8 * 8;
   const unsigned grid = a.slots ? a.slots : (unsigned)(units * a.col_tiles);
   hipLaunchKernelGGL(bf ? prefill_kernel<true>(D, groups) : prefill_kernel<false>(D, groups),
-                     dim3(grid), dim3(256), 0, st, a);
+                     kv4_grid(grid), dim3(256), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.slots == 0) return e;
   auto join = D == 128 ? (bf ? kv4_prefill_join_kernel<128, true> : kv4_prefill_join_kernel<128, false>)
