@@ -40,3 +40,22 @@ def test_attention_of_a_long_prompt_among_many_sequences(lib):
     few[700] = 256
     small = run(list(range(batch)), few, torch.cat([q[:956], q[700 + long:]]))
     assert torch.equal(small[:700], out[:700]) and torch.equal(small[956:], out[700 + long:])
+
+
+def test_norm_of_more_rows_than_a_grid_has_places(lib):
+    M, K, part = (1 << 24) + 70, 8, 1 << 19
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, gamma = torch.randn(M, K, generator=g, device="cuda").half(), torch.randn(K, generator=g, device="cuda").half()
+
+    def run(x):
+        y8, y = torch.empty(x.shape, dtype=torch.uint8, device="cuda"), torch.full_like(x, float("nan"))
+        s = torch.full((x.shape[0],), float("nan"), device="cuda")
+        lib.w4a8_rmsnorm(x, None, gamma, None, y8, s, y, x.shape[0], K, 1e-5, lib.DT_F16)
+        torch.cuda.synchronize()
+        return y8, s, y
+
+    whole = run(x)
+    for at in (0, part, (1 << 20) - 100, 1 << 20, 5 << 20, M - part):
+        for a, b in zip(whole, run(x[at:at + part])):
+            assert torch.equal(a[at:at + part], b), at
+    assert whole[1].isfinite().all() and whole[2].isfinite().all()

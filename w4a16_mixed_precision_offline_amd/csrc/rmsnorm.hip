@@ -33,11 +33,11 @@ constexpr float kLeastMean = 0x1p-80f, kLeastTop = 0x1p-100f, kLeastScale = 0x1p
 template <int T, bool BF>
 __device__ __forceinline__ void wide_row(const u32x4v* X, const u32x4v* R, const u32x4v* gamma,
                                          const u32x4v* H, u32x2v* Y8, float* yscale, u32x4v* Y,
-                                         int K, float eps) {
+                                         unsigned m, int K, float eps) {
   constexpr int NW = T / 64;
   __shared__ double red[NW][2];
   const int tid = threadIdx.x, pairs = K / 2;
-  const size_t row = (size_t)blockIdx.x * pairs;
+  const size_t row = (size_t)m * pairs;
   const uint32_t* x = reinterpret_cast<const uint32_t*>(H != nullptr ? H : X) + row;
   const uint32_t* r = H != nullptr || R == nullptr ? nullptr
                                                    : reinterpret_cast<const uint32_t*>(R) + row;
@@ -82,7 +82,7 @@ __device__ __forceinline__ void wide_row(const u32x4v* X, const u32x4v* R, const
   } else if (exact == INFINITY) {
     up = 0.;
   }
-  if (tid == 0) yscale[blockIdx.x] = s;
+  if (tid == 0) yscale[m] = s;
 #pragma unroll 1
   for (int c = tid; c < pairs; c += T) {
     const uint32_t h = h_pair(c);
@@ -96,18 +96,23 @@ __device__ __forceinline__ void wide_row(const u32x4v* X, const u32x4v* R, const
   }
 }
 
+// Rows past the first 2^20 lie in further rows of the grid, whose dimensions take 2^32 threads.
+constexpr unsigned kGridRow = 1u << 20;
+
 // T threads, CH 16-byte chunks of a row in each.
 template <int T, int CH, bool BF>
 __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4v* R,
                                                     const u32x4v* __restrict__ gamma, u32x4v* H,
                                                     u32x2v* __restrict__ Y8,
-                                                    float* __restrict__ yscale, u32x4v* Y, int K,
-                                                    float eps) {
+                                                    float* __restrict__ yscale, u32x4v* Y, int M,
+                                                    int K, float eps) {
   constexpr int NW = T / 64;
   __shared__ float red[NW][2];
   const int tid = threadIdx.x;
   const int chunks = K / 8;
-  const size_t row = (size_t)blockIdx.x * chunks;
+  const unsigned m = blockIdx.x + blockIdx.y * kGridRow;
+  if (m >= (unsigned)M) return;
+  const size_t row = (size_t)m * chunks;
   u32x4v h[CH], gm[CH];
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
@@ -187,11 +192,11 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4
   const bool narrow = ss < INFINITY && mean >= kLeastMean && top >= kLeastTop &&
                       s >= kLeastScale && s < INFINITY;
   if (__ballot(!narrow) != 0) {
-    wide_row<T, BF>(X, R, gamma, H, Y8, yscale, Y, K, eps);
+    wide_row<T, BF>(X, R, gamma, H, Y8, yscale, Y, m, K, eps);
     return;
   }
   const float up = 448.f / top;
-  if (tid == 0) yscale[blockIdx.x] = s;
+  if (tid == 0) yscale[m] = s;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int c = tid + j * T;
@@ -217,7 +222,7 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4
 }
 
 typedef void (*NormFn)(const u32x4v*, const u32x4v*, const u32x4v*, u32x4v*, u32x2v*, float*,
-                       u32x4v*, int, float);
+                       u32x4v*, int, int, float);
 template <bool BF>
 NormFn norm_kernel(int threads, int ch) {
   if (threads == 256)
@@ -240,10 +245,11 @@ hipError_t launch_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* 
   const int threads = chunks <= 1024 ? 256 : 1024;
   const int ch = (chunks + threads - 1) / threads;
   NormFn fn = bf ? norm_kernel<true>(threads, ch) : norm_kernel<false>(threads, ch);
-  hipLaunchKernelGGL(fn, dim3(M), dim3(threads), 0, st, reinterpret_cast<const u32x4v*>(X),
+  const dim3 grid = (unsigned)M <= kGridRow ? dim3(M) : dim3(kGridRow, (M - 1) / kGridRow + 1);
+  hipLaunchKernelGGL(fn, grid, dim3(threads), 0, st, reinterpret_cast<const u32x4v*>(X),
                      reinterpret_cast<const u32x4v*>(R), reinterpret_cast<const u32x4v*>(gamma),
                      reinterpret_cast<u32x4v*>(H), reinterpret_cast<u32x2v*>(Y8), yscale,
-                     reinterpret_cast<u32x4v*>(Y), K, eps);
+                     reinterpret_cast<u32x4v*>(Y), M, K, eps);
   return hipGetLastError();
 }
 
