@@ -87,3 +87,22 @@ def test_infinite_and_nan_rows_of_any_magnitude(lib):
     H, Y8, S, Y = run_norm(lib, x, None, g, 1e-5)
     assert (S[:5] == 1).all() and S[5] != 1
     assert Y8[3:5].isnan().all() and torch.equal(Y8[:3].isnan(), x[:3].isinf()) and (Y8[:3].nan_to_num() == 0).all()
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("K", [8, 4096, 16384, 65536])
+def test_rows_of_zeros_among_others(lib, K, t):
+    least = torch.tensor([1], dtype=torch.int16).view(t)  # squares to 0 in fp32, for bf16
+    x, g = rand(11, 6, K, t=t), rand(12, K, t=t)
+    x[0] = x[3] = 0
+    x[2] = x[4] = x[5] = -0.0
+    x[4, K - 1] = x[5, 0] = least[0]
+    for eps in (0.0, 1e-5):
+        H, Y8, S, Y = run_norm(lib, x, None, g, eps)
+        for m in (0, 2, 3):
+            assert S[m] == 1 and (Y8[m] == 0).all() and (Y[m] == 0).all()
+        if eps == 0:
+            keep = torch.tensor([1, 4, 5])
+            _, y, s = ref.norm(x[keep], None, g, eps)
+            assert ((S[keep].double() - s).abs() <= REL * s).all()
+            assert ((Y[keep].double() - y).abs() <= (ref.half_step(t) + REL) * y.abs() + 2.0 ** -25).all()

@@ -9,8 +9,8 @@
 // y / s = (h g) * (448 / max|h g|), which needs no norm at all.  Sums are fp32.
 //
 // bf16 rows can leave the fp32 range, their squares above and below, their products with g
-// too: such rows, and those of zeros, are worked out again in 64 bits, where nothing of
-// theirs can.  True infinities and NaN end as the formula ends: a NaN makes the row's codes
+// too: such rows are worked out again in 64 bits, where nothing of theirs can, in twice the
+// time.  True infinities and NaN end as the formula ends: a NaN makes the row's codes
 // NaN, an infinity is a NaN among zeros, and s = 1 for both.
 //
 // Bound: HBM.  8192 x 8192 fp16: 470 MB in 79 us, 5.9 TB/s (a large copy: 4.9); one row of
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4
                                                     float* __restrict__ yscale, u32x4v* Y, int M,
                                                     int K, float eps) {
   constexpr int NW = T / 64;
-  __shared__ float red[NW][2];
+  __shared__ float red[NW][3];
   const int tid = threadIdx.x;
   const int chunks = K / 8;
   const unsigned m = blockIdx.x + blockIdx.y * kGridRow;
@@ -186,23 +186,42 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const u32x4v* X, const u32x4
   float ss, top;
   reduce(ss, top);
   const float mean = ss / (float)K + eps;
-  const float inv = rsqrtf(mean);
-  const float s = inv * top * (1.f / 448.f);
-  // the same for the whole workgroup (the ballot shows it to the compiler)
+  float inv = rsqrtf(mean);
+  float s = inv * top * (1.f / 448.f);
+  float up = 448.f / top;
+  // All of this is the same for the whole workgroup (the ballots show it to the compiler).
+  // A sum of 0 is a row of zeros, as padding has them, or one too small for fp32.
+  bool zeros = false;
+  if (__ballot(ss == 0.f) != 0) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) bits |= h[j][0] | h[j][1] | h[j][2] | h[j][3];
+    const bool some = __ballot((bits & 0x7FFF7FFFu) != 0) != 0;
+    if ((tid & 63) == 0) red[tid >> 6][2] = some ? 1.f : 0.f;
+    __syncthreads();
+    float any = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) any += red[w][2];
+    zeros = __ballot(any == 0.f) != 0;
+  }
   const bool narrow = ss < INFINITY && mean >= kLeastMean && top >= kLeastTop &&
                       s >= kLeastScale && s < INFINITY;
-  if (__ballot(!narrow) != 0) {
+  if (zeros) {
+    inv = 0.f;
+    up = s = 1.f;
+  } else if (__ballot(!narrow) != 0) {
     wide_row<T, BF>(X, R, gamma, H, Y8, yscale, Y, m, K, eps);
     return;
   }
-  const float up = 448.f / top;
   if (tid == 0) yscale[m] = s;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int c = tid + j * T;
     if (c >= chunks) continue;
-    // unpacked again: the compiler would hold all of h g since the sums, twice the registers
+    // Unpacked again: the compiler would hold what it has unpacked since the sums.  Gamma too
+    // only where registers would spill; with 256 threads, 8192 x 8192, 81.4 us instead of 80.6.
     asm("" : "+v"(h[j]));
+    if constexpr (T == 1024) asm("" : "+v"(gm[j]));
     float a[8], g[8], y[8];
     unpack8<BF>(h[j], a);
     unpack8<BF>(gm[j], g);
