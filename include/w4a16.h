@@ -430,20 +430,23 @@ size_t w4a16_lora_workspace_bytes(int M, int N, int K, int rank);
  *   lens  (device) int32 [batch]: tokens of each sequence, the new ones included, so the last
  *     new one is at position lens[b] - 1.
  *   max_new: at least the most new tokens of a sequence; what a sequence has beyond is
- *     left alone.  Values of rows outside 0 .. tokens are brought into that range.
+ *     left alone.  Values of rows outside 0 .. tokens are brought into that range.  Rows of no
+ *     sequence are not read, and keep what they held where a call writes rows.
  * w4a16_kv4_append: quantizes the new tokens' k and v ([tokens] rows of kv_heads * head, ldk
  *   and ldv apart) into their pages; every other token keeps its bits.  Two sequences may
  *   share pages of the table that neither writes.  Tokens without a page, or at a negative
  *   position, are dropped.
  * w4a16_kv4_gather: the other way, the values of the same tokens as rows of k and v, rounded to
- *   dtype; zeros where there is no page.  With lens = the lengths and rows their running
+ *   dtype; zeros where there is no page.  The rows of tokens at a negative position are left
+ *   alone.  With lens = the lengths and rows their running
  *   sums it reads whole sequences.
  * w4a16_kv4_attention: out = softmax(scale * q k^T) v of each new token over the cached ones
  *   (append them first): token t of position p is seen if t <= p, t > p - window
  *   (window > 0 only) and it has a page.  q (device, in) and out (device, out): [tokens] rows
  *   of q_heads * head, ldq and ldo apart; query head h reads kv head h / (q_heads / kv_heads).
  *   lse (device, out) fp32 [tokens][q_heads], may be NULL: the natural logarithm of the sum
- *   of exp(scale * q k).  A token that sees nothing gets out 0 and lse -infinity.  What the
+ *   of exp(scale * q k).  A token that sees nothing gets out 0 and lse -infinity.  scale
+ *   is above 0, and 1.45 scale * q k has to lie in the fp32 range.  What the
  *   pages hold in places that no token sees does not matter; a NaN reaches every token that
  *   sees it, and may reach other new tokens of its sequence.  max_len: at least the
  *   longest of lens (a longer one is still right, but slow).  The tokens are divided between

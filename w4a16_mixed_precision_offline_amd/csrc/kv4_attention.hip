@@ -30,15 +30,19 @@
 // The blocks of all tiles are cut into equal stripes, one for each of the workgroups that
 // the card holds at once; the sums of a tile that stripes share are joined in order.
 //
-// Bound: HBM for large caches, latency for small ones.  48 requests to 8192 tokens, 64 query
-// heads on 8 of 128 channels, groups of 64: 234 MB in 50 us, 4.7 TB/s (a large copy: 4.9; 58 us
-// where nothing is left in the 256 MiB cache of an earlier pass); contexts of 131072 and 16538
-// tokens, groups of 32: 189 MB in 50 us (66 us); 3999 tokens of 32 heads: 17 MB in 12.9 us, of
-// which 0.7 us find the part, 1.5 us load q, 2.4 us stream 2 blocks a wave, 1.8 us hand the
-// sums over and 3 us join them.  512 stripes, two to a compute unit, which is what the
-// registers allow: 256 / 768 / 1024 take 59 / 60 / 57 us on the first and 58 / 76 / 87 on the
-// second (50.8 with 512).  Equal stripes without the `lead` of a tile: 75 us on the first.
-// Tiles of 8 columns against 16 where both fit: 49.9 against 56.7 us on the first.
+// Bound: loads in flight for large caches, latency for small ones.  48 requests to 8192 tokens,
+// 64 query heads on 8 of 128 channels, groups of 64: 234 MB in 59 us, 4.0 TB/s (a plain read:
+// 6.3; 50 us with what the 256 MiB cache keeps of an earlier pass over the same bytes); contexts
+// of 131072 and 16538 tokens, groups of 32: 189 MB in 66 us, 2.9 TB/s (51 us); 3999 tokens of 32
+// heads: 17 MB in 13.1 us, of which 0.7 us find the part, 1.5 us load q, 2.4 us stream 2 blocks
+// a wave, 1.8 us hand the sums over and 3 us join them.  512 stripes, two to a compute unit,
+// which is what the registers allow: over the same bytes again 256 / 512 / 768 / 1024 take 59 /
+// 50 / 60 / 57 us on the first and 58 / 51 / 76 / 87 on the second.  Equal stripes without the
+// `lead` of a tile: 75 us on the first.  Tiles of 8 columns against 16 where both fit: 50
+// against 57 us on the first.
+// Registers: 193 to 227 with 128 channels, two waves to a SIMD.  With groups of 32 the two
+// blocks and their s and m do not fit into 256: 17 are spilled in tiles of 8, 41 to 45 in tiles
+// of 16.  56 to 84 scalar registers of the division into stripes lie in vector registers.
 #include "kv4_attend.h"
 
 namespace w4a16 {
@@ -567,6 +571,11 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
   if (window > 0 && span > ((long long)window + p.cols / ratio + 1) / 32 + 2)
     span = ((long long)window + p.cols / ratio + 1) / 32 + 2;
   if (p.cols == 128) {
+    // Chunks of 8 / 16 / 32 blocks at least, us: 32 new tokens of 8 sequences on 2 kv heads, to
+    // 16384: 55 / 47 / 56; 200 on 4, 2000: 33 / 35 / 49; 64 of 4 on 8, to 4096: 65 / 65 / 60;
+    // 1024 on 1, 1024: 26 / 32 / 47; no difference above.  Chunks for 256 / 512 / 768 / 1024
+    // workgroups: 512 on 8, 8192: 296 / 244 / 254 / 250; 512 of 2 on 1, 16384: 163 / 142 / 111 /
+    // 129; 130 on 8, 131072: 1843 / 1432 / 1286 / 1207.
     p.target = KV4_STRIPES;
     p.chunk = 16;
     p.chunks = (int)((span + p.chunk - 1) / p.chunk);
@@ -579,6 +588,10 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     p.slots = (int)slots;
     p.tiles = (int)tiles;
   } else {
+    // Stripes of 4 / 8 / 16 / 32 blocks at least, single tokens, us: one sequence of 1000 tokens
+    // on 8 kv heads 9.5 / 10.2 / 11.7 / 11.5, of 4000 13.8 / 11.6 / 11.8 / 14.8, of 16000 25.4 /
+    // 25.9 / 16.5 / 16.6; six to 4000 15.9 / 15.2 / 12.5 / 15.3, to 16000 26 each; 24 to 1000
+    // 16.1 / 16.1 / 16.0 / 12.5, to 16000 55 each.
     p.chunk = 8;
     long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
     if (batch > 1024 || stripes <= tiles) return p;

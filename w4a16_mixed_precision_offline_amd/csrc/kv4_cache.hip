@@ -9,7 +9,7 @@
 // instead: the same words go through LDS and an 8 x 8 transposition of nibbles in registers.
 //
 // Bound: HBM and vector instructions.  Prompts of 9 requests (13807 tokens, 8 kv heads of 128
-// bf16 channels): 25 us written (74 MB, 3.0 TB/s; a large copy: 4.9), 17 us read back (4.3
+// bf16 channels): 25 us written (74 MB, 3.0 TB/s; a large copy: 4.9, a sum of two arrays: 5.9), 17 us read back (4.3
 // TB/s); one token of each of 64 requests: 5.7 us and 3.6 us, chains of dependent loads.  The
 // quotient by the divider for every code took 28 us and 8.4 us.
 #include "kv4.h"

@@ -18,15 +18,15 @@
 //
 // For fp16 rows p is hi + lo, 22 bits, as with the smaller tiles, at 8 matrix instructions
 // more on 17: with p rounded once the result's error is 1.65 times that of its own rounding,
-// with lo 1.33 times, and 4 sequences of 512 new tokens take 625 us instead of 480.  bf16
-// rows, whose own step is 2^-9, do without.
+// with lo 1.33 times, and 4 sequences of 512 new tokens take 611 us instead of 480.  bf16
+// rows, whose own step is 2^-9, do without (424 us).
 //
 // Bound: matrix and vector instructions together.  4 sequences of 4109 to 8192 tokens, 512
-// of them new, 64 query heads on 8 of 128 channels: 370 GFLOP in 625 us, 0.59 PFLOP/s, half
-// of the rate of a large fp16 product (1.2 PFLOP/s), 1060 us with tiles of 16.  Counters: the
-// matrix unit busy 47% and the vector unit 52% of the time, LDS 28%; two waves of 210 to 240
-// registers fit a SIMD and take turns badly.  Measured, not kept: one block's
-// product issued beside the exponentials of the block before it (with p hi + lo 640 us,
+// of them new, 64 query heads on 8 of 128 channels: 370 GFLOP in 611 us (601 to 634 from card
+// to card), 0.61 PFLOP/s, half of the rate of a large fp16 product (1.2 PFLOP/s), 1060 us with
+// tiles of 16.  Counters: the matrix unit busy 45% and the vector unit 51% of the time, LDS 27%;
+// two waves of 208 to 240 registers fit a SIMD and take turns badly.  Measured, not kept: one
+// block's product issued beside the exponentials of the block before it (with p hi + lo 640 us,
 // registers spill), two sums per product instead of one dependent chain (637 us), longest
 // sequences first (no difference).
 #include "kv4_attend.h"

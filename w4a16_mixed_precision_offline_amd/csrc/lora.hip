@@ -18,11 +18,14 @@
 // largest |T| in [1, 2), so that neither overflow nor underflow touches it), 16 bits in
 // bf16, whose own step is 2^-9.
 //
-// Bound: HBM for many rows, latency for few.  4096 rows, 8192 x 8192, rank 64: 69 us for
-// 201 MB of X, base and Y, 2.9 TB/s (a large copy: 4.9): X A^T 29 us (67 MB, its loads four
-// steps at a time; 37 us one at a time), the split 5 us, T B^T 35 us (134 MB).  48 rows with
-// 40 adapters of rank 16, 8192 x 10240: 14 us; one row, 4096 x 4096: 8.3 us, two launches.
-// Measured, not kept: the slices joined by the last workgroup to arrive (4096 rows 80 us).
+// Bound: HBM for many rows, latency for few.  4096 rows, 8192 x 8192, rank 64: 79 us a call for
+// 201 MB of X, base and Y, 2.5 TB/s (a sum of two arrays: 5.9): X A^T 28 us (67 MB, its loads
+// four steps at a time; 37 us one at a time), the split 5 us, T B^T 36 us (134 MB).  48 rows
+// with 40 adapters of rank 16, 8192 x 10240: 6.2 and 8.0 us in the kernels, 15.2 a call; one row,
+// 4096 x 4096: 3.3 and 3.9 us, 9.7 a call.  2048 rows of rank 128: 88 us (39, 9 and 35): X A^T
+// with 128 KiB of LDS, one workgroup to a compute unit, T B^T with 20 to 23 registers spilled.
+// Measured, not kept: the slices joined by the last workgroup to arrive (the kernels of 4096
+// rows together 80 us instead of 69).
 #include "internal.h"
 #include "rows16.h"
 
@@ -422,7 +425,7 @@ LoraPlan lora_make_plan(int M, int N, int K, int rank) {
                           (K + p.kslice - 1) / p.kslice > 16))
     p.kslice *= 2;
   p.slices = (K + p.kslice - 1) / p.kslice;
-  // 4096 rows: 67 us with pieces of 512, 70 with 256 and with 1024
+  // 4096 rows, the three kernels: 67 us with pieces of 512, 70 with 256 and with 1024
   p.ncols = 256;
   while (p.ncols < 512 && (long long)p.tiles * ((N + 2 * p.ncols - 1) / (2 * p.ncols)) >= 512)
     p.ncols *= 2;

@@ -13,8 +13,8 @@
 // time.  True infinities and NaN end as the formula ends: a NaN makes the row's codes
 // NaN, an infinity is a NaN among zeros, and s = 1 for both.
 //
-// Bound: HBM.  8192 x 8192 fp16: 470 MB in 79 us, 5.9 TB/s (a large copy: 4.9); one row of
-// 4096: 2.5 us in the kernel, 5.3 us a call.
+// Bound: HBM.  8192 x 8192 fp16: 470 MB in 81 us, 5.8 TB/s (a sum of two arrays: 5.9); 4096 x
+// 65536 bf16: 373 us, 5.0 TB/s; one row of 4096: 2.6 us in the kernel, 5.6 us a call.
 #include "internal.h"
 #include "rows16.h"
 
@@ -259,8 +259,9 @@ hipError_t launch_rmsnorm(const uint16_t* X, const uint16_t* R, const uint16_t* 
                           hipStream_t st) {
   if (M <= 0 || K <= 0 || K % 8 != 0 || K > NORM_MAX_K) return hipErrorInvalidValue;
   const int chunks = K / 8;
-  // 4096 rows of 4096 / 8192 values: 18.7 / 34.8 us with 256 threads, 23.8 / 37.7 with 1024; past
-  // 8192 values 256 threads would need more than 4 chunks each
+  // 4096 rows of 4096 / 8192 values: 18.7 / 34.8 us with 256 threads, 23.8 / 37.7 with 1024; 1024
+  // rows of 8192: 11.2 / 12.7; 256 rows of 4096: 5.8 / 5.3; 1 to 64 rows: 5.7 / 5.7.  Past 8192
+  // values 256 threads would need more than 4 chunks each
   const int threads = chunks <= 1024 ? 256 : 1024;
   const int ch = (chunks + threads - 1) / threads;
   NormFn fn = bf ? norm_kernel<true>(threads, ch) : norm_kernel<false>(threads, ch);
