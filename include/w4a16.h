@@ -450,7 +450,9 @@ size_t w4a16_lora_workspace_bytes(int M, int N, int K, int rank);
  *   pages hold in places that no token sees does not matter; a NaN reaches every token that
  *   sees it, and may reach other new tokens of its sequence.  max_len: at least the
  *   longest of lens (a longer one is still right, but slow).  The tokens are divided between
- *   workgroups by the lengths on the device, the same way every time.  The workspace
+ *   workgroups by the lengths on the device, the same way every time, in tiles as wide as
+ *   max_new asks for: single tokens with long contexts belong in a call of their own rather
+ *   than beside a prompt.  The workspace
  *   (w4a16_kv4_workspace_bytes; 0 for an invalid shape, and where none is needed) is the
  *   stream's, under the rules of w4a16_gemm; its arrival counters are left at zero.  As with
  *   w4a16_lora one call before a capture covers the smaller ones, here all of the same head

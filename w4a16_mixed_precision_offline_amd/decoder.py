@@ -97,7 +97,8 @@ class Kv4Cache(torch.nn.Module):
     def attend(self, q: torch.Tensor, batch: Batch, q_heads: int, window: int = 0, scale: float | None = None,
                lse: torch.Tensor | None = None) -> torch.Tensor:
         """Attention of the new tokens q [tokens, q_heads * head] over the cached ones.  Rows of
-        no sequence (padding, new tokens past batch.max_new) are 0; in lse they keep what they held."""
+        no sequence (padding, new tokens past batch.max_new) are 0; in lse they keep what they held.
+        Single tokens with long contexts are faster in a batch of their own than beside a prompt."""
         ldq = _rows16("q", q, q_heads * self.head)
         if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (q.shape[0], q_heads) or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous float32 tensor of shape {(q.shape[0], q_heads)}")
