@@ -3,8 +3,9 @@ moved, saved or trained: host code only, nothing here reaches a kernel."""
 import pytest
 import torch
 
-from w4a16_mixed_precision_offline_amd.decoder import Adapters, AttentionBlock, Batch, Kv4Cache
-from w4a16_mixed_precision_offline_amd.layer import W4A16Linear
+pytest.importorskip("w4a16_mixed_precision_offline_amd")
+from w4a16_mixed_precision_offline_amd.decoder import Adapters, AttentionBlock, Batch, Kv4Cache  # noqa: E402
+from w4a16_mixed_precision_offline_amd.layer import W4A16Linear  # noqa: E402
 
 
 def half(*shape):
