@@ -476,6 +476,102 @@ int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* l
 size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len, int q_heads,
                                  int kv_heads, int head, int window);
 
+/* Trees of drafted tokens over the 4-bit cache.  A step that checks drafted tokens appends all
+ * nodes of a sequence's tree to its end, node j (counted from 0 within the sequence) as the token
+ * behind the `held` ones, at place held + j = lens - new + j; rows, lens, max_new and table are
+ * those of w4a16_kv4_append.  The step attends with a mask (each node sees what the cache held
+ * before and its own ancestors), keeps one branch, moves its tokens together and gives the pages
+ * of the others back.
+ * w4a16_kv4_tree: from the parents, what the others take.
+ *   parent (device, in) int32 [tokens]: the node that the row's token follows, counted within its
+ *     sequence; what is below 0, or not below the node itself, means that it follows the last
+ *     token held.
+ *   mask  (device, out) uint32 [tokens][words]: bit j % 32 of word j / 32: the token follows node
+ *     j, or is it.  window > 0 keeps the nearest `window` of these.  32 * words >= max_new.
+ *   depth (device, out) int32 [tokens], may be NULL: nodes before it on its branch.
+ *   pos   (device, out) int32 [tokens], may be NULL: its position, held + depth, for w4a16_rotary.
+ *   max_new <= 4096.  Rows of no sequence keep what they held in all three.
+ * w4a16_kv4_tree_attention: w4a16_kv4_attention with another rule of what is seen.  A node sees
+ *   the tokens t < held that have a page (window > 0: t > held + depth - window) and the nodes
+ *   that its bits name, itself only if they do; bits of nodes that the sequence does not have, and
+ *   nodes past the mask's words, are not seen.  Any bits are allowed, a causal row among them.
+ *   depth is read with window > 0 only (else it may be NULL), and brought into 0 .. nodes - 1.
+ *   A node that sees nothing gets out 0 and lse -infinity.  Everything else is as there, the
+ *   workspace too (w4a16_kv4_tree_workspace_bytes).
+ * w4a16_kv4_compact: the tokens of the accepted nodes move to the front of the tree's place, in
+ *   every layer: node path[b][j] goes to place held + j, j = 0 .. count[b] - 1, all of them as they
+ *   were before the call.
+ *   path (device, in) int32 [batch][max_path], ascending along the branch, so path[j] >= j; an
+ *     entry that is not, or is no node of the sequence, is left out (its place keeps its token),
+ *     and so is one whose place or node has no page.  count (device, in) int32 [batch], brought
+ *     into 0 .. min(max_path, nodes).
+ *   lens_out (device, out) int32 [batch]: held + count; must not overlap lens.
+ *   The pool: `layers` caches of one layout, layer_bytes apart (any multiple of 16 that holds
+ *   `pages` pages; not looked at with one layer), all with the same table.  Pages that are
+ *   written must not be shared.  layers * kv_heads <= 2^20.
+ * w4a16_kv4_fork: who has which pages in the next step: forks sequences, ends them, takes tokens
+ *   back, makes room, and frees what nobody holds any more.  New row r goes on from old row
+ *   parent[r] (below 0 or >= batch: a new sequence, with nothing) and keeps its first keep[r]
+ *   tokens (keep NULL: all; more than it has: all); it has pages for room[r] tokens in all (room
+ *   NULL or less: for the ones kept).
+ *   Pages kept whole are shared with whoever else keeps them.  A last page of which only a part is
+ *   kept stays with the row, except that where it is pinned, or kept whole by another row, or
+ *   several rows go on in it, all but the lowest row of the last get a page of their own, and the
+ *   tokens kept are copied to it in every layer.  Pages that no new row keeps and that are not
+ *   pinned are free, and are given out from the lowest number up, to the rows in their order.
+ *   table (device, in) int32 [batch][width] and lens (device, in) int32 [batch]: of the old rows.
+ *   pinned (device, in) uint8 [pages], may be NULL: not 0: never given out (pages that
+ *     something beside the table holds), nor written.
+ *   table_out (device, out) int32 [batch_out][width]: -1 where there is no page; lens_out (device,
+ *     out) int32 [batch_out]: the tokens kept.  Neither may overlap table or lens.
+ *   missing (device, out) int32 [1], may be NULL: how many pages there were too few; the last
+ *     entries that were due are -1 then, the kept tokens of a copied page among them.  The old
+ *     table and its pages are as they were, so the call can be made again with fewer rows.
+ *   Old rows must not list a page twice; keep and room are cut off at width * page tokens.
+ *   batch_out <= 2048, pages <= 2^19; the pool is that of w4a16_kv4_compact. */
+int w4a16_kv4_tree(const int32_t* parent, const int32_t* rows, const int32_t* lens, uint32_t* mask,
+                   int32_t* depth, int32_t* pos, int batch, int tokens, int max_new, int words,
+                   int window, void* stream);
+int w4a16_kv4_tree_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
+                             const int32_t* table, const void* cache, const uint32_t* mask,
+                             const int32_t* depth, uint16_t* out, float* lse, int batch,
+                             int tokens, int max_new, int max_len, int words, int ldq, int ldo,
+                             int q_heads, int kv_heads, int head, int group, int page, int pages,
+                             int width, int window, float scale, int dtype, void* stream);
+size_t w4a16_kv4_tree_workspace_bytes(int batch, int tokens, int max_new, int max_len, int q_heads,
+                                      int kv_heads, int head, int window);
+int w4a16_kv4_compact(void* cache, const int32_t* path, const int32_t* count, const int32_t* rows,
+                      const int32_t* lens, const int32_t* table, int32_t* lens_out, int batch,
+                      int tokens, int max_new, int max_path, int layers, size_t layer_bytes,
+                      int kv_heads, int head, int group, int page, int pages, int width,
+                      void* stream);
+int w4a16_kv4_fork(void* cache, const int32_t* table, const int32_t* lens, const int32_t* parent,
+                   const int32_t* keep, const int32_t* room, const uint8_t* pinned,
+                   int32_t* table_out, int32_t* lens_out, int32_t* missing, int batch,
+                   int batch_out, int layers, size_t layer_bytes, int kv_heads, int head, int group,
+                   int page, int pages, int width, void* stream);
+
+/* w4a16_rotary: rotary positions of queries and keys, in one call.  Pair i of a head's first `rot`
+ *   channels is turned by w = pos[axis[i]][t] * freq[i]:
+ *     (a, b) -> (a cos w - b sin w, b cos w + a sin w)
+ *   pairs W4A16_ROTARY_HALVES: channels i and i + rot / 2; W4A16_ROTARY_NEIGHBOURS: 2 i, 2 i + 1.
+ *   q (device, in), qo (device, out): [tokens] rows of q_heads * head, ldq and ldqo apart; k and ko
+ *     likewise of kv_heads (kv_heads 0: both may be NULL).  qo may be q and ko k (in place, with
+ *     the same distance of rows); they must not overlap otherwise.  Channels past rot are copied.
+ *   pos (device, in) int32 [axes], ldpos apart, of [tokens]: positions on each axis (time, height,
+ *     width); axis (device, in) int32 [rot / 2]: the axis of each frequency, brought into
+ *     0 .. axes - 1, may be NULL with one axis; freq (device, in) fp32 [rot / 2], radians per
+ *     position; with -freq the rotation is undone, which is also its gradient.
+ *   Angles are formed in 64 bits, so positions may be any int32; the rest is fp32 and each result
+ *   is rounded once.  16 <= rot <= head <= 512, rot % 16 == 0, head % 8 == 0, tokens <= 2^25,
+ *   (q_heads + kv_heads) * head <= 2^24. */
+#define W4A16_ROTARY_HALVES     0
+#define W4A16_ROTARY_NEIGHBOURS 1
+int w4a16_rotary(const uint16_t* q, const uint16_t* k, const int32_t* pos, const int32_t* axis,
+                 const float* freq, uint16_t* qo, uint16_t* ko, int tokens, int q_heads,
+                 int kv_heads, int head, int rot, int axes, int ldpos, int ldq, int ldk, int ldqo,
+                 int ldko, int pairs, int dtype, void* stream);
+
 /* ---- calibration kernels (measurement only) ---------------------------------------
  * The achievable ceilings the GEMM's rates are set against, beside the published peaks.
  * w4a16_probe_read: one plain streaming read of `bytes` bytes at device pointer p

@@ -74,6 +74,12 @@ _SIGS = {
     "w4a16_kv4_gather": (_I, [_P] * 6 + [_I] * 12 + [_P]),
     "w4a16_kv4_attention": (_I, [_P] * 7 + [_I] * 14 + [_F, _I, _P]),
     "w4a16_kv4_workspace_bytes": (_SZ, [_I] * 8),
+    "w4a16_kv4_tree": (_I, [_P] * 6 + [_I] * 5 + [_P]),
+    "w4a16_kv4_tree_attention": (_I, [_P] * 9 + [_I] * 15 + [_F, _I, _P]),
+    "w4a16_kv4_tree_workspace_bytes": (_SZ, [_I] * 8),
+    "w4a16_kv4_compact": (_I, [_P] * 7 + [_I] * 5 + [_SZ] + [_I] * 6 + [_P]),
+    "w4a16_kv4_fork": (_I, [_P] * 10 + [_I] * 3 + [_SZ] + [_I] * 6 + [_P]),
+    "w4a16_rotary": (_I, [_P] * 7 + [_I] * 13 + [_P]),
     "w4a16_probe_read": (_I, [_P, _SZ, _P, _P]),
     "w4a16_probe_mfma": (_I, [_I, _I, _P, _P]),
     "w4a16_probe_mfma_flops": (ctypes.c_double, [_I, _I]),
@@ -363,6 +369,56 @@ def w4a16_kv4_workspace_bytes(batch: int, tokens: int, max_new: int, max_len: in
                               kv_heads: int, head: int, window: int = 0) -> int:
     return _lib.w4a16_kv4_workspace_bytes(batch, tokens, max_new, max_len, q_heads, kv_heads, head,
                                           window)
+
+
+def w4a16_kv4_tree(parent, rows, lens, mask, depth, pos, batch, tokens, max_new, words, window=0,
+                   stream=None):
+    _check("w4a16_kv4_tree", _lib.w4a16_kv4_tree(
+        _ptr(parent), _ptr(rows), _ptr(lens), _ptr(mask), _ptr(depth), _ptr(pos), batch, tokens,
+        max_new, words, window, _stream(stream)))
+
+
+def w4a16_kv4_tree_attention(q, rows, lens, table, cache, mask, depth, out, lse, batch, tokens,
+                             max_new, max_len, words, ldq, ldo, q_heads, kv_heads, head, group,
+                             page, pages, width, window, scale, dtype=DT_F16, stream=None):
+    _check("w4a16_kv4_tree_attention", _lib.w4a16_kv4_tree_attention(
+        _ptr(q), _ptr(rows), _ptr(lens), _ptr(table), _ptr(cache), _ptr(mask), _ptr(depth),
+        _ptr(out), _ptr(lse), batch, tokens, max_new, max_len, words, ldq, ldo, q_heads, kv_heads,
+        head, group, page, pages, width, window, scale, dtype, _stream(stream)))
+
+
+def w4a16_kv4_tree_workspace_bytes(batch: int, tokens: int, max_new: int, max_len: int,
+                                   q_heads: int, kv_heads: int, head: int, window: int = 0) -> int:
+    return _lib.w4a16_kv4_tree_workspace_bytes(batch, tokens, max_new, max_len, q_heads, kv_heads,
+                                               head, window)
+
+
+def w4a16_kv4_compact(cache, path, count, rows, lens, table, lens_out, batch, tokens, max_new,
+                      max_path, layers, layer_bytes, kv_heads, head, group, page, pages, width,
+                      stream=None):
+    _check("w4a16_kv4_compact", _lib.w4a16_kv4_compact(
+        _ptr(cache), _ptr(path), _ptr(count), _ptr(rows), _ptr(lens), _ptr(table), _ptr(lens_out),
+        batch, tokens, max_new, max_path, layers, layer_bytes, kv_heads, head, group, page, pages,
+        width, _stream(stream)))
+
+
+def w4a16_kv4_fork(cache, table, lens, parent, keep, room, pinned, table_out, lens_out, missing,
+                   batch, batch_out, layers, layer_bytes, kv_heads, head, group, page, pages, width,
+                   stream=None):
+    _check("w4a16_kv4_fork", _lib.w4a16_kv4_fork(
+        _ptr(cache), _ptr(table), _ptr(lens), _ptr(parent), _ptr(keep), _ptr(room), _ptr(pinned),
+        _ptr(table_out), _ptr(lens_out), _ptr(missing), batch, batch_out, layers, layer_bytes,
+        kv_heads, head, group, page, pages, width, _stream(stream)))
+
+
+ROTARY_HALVES, ROTARY_NEIGHBOURS = range(2)  # W4A16_ROTARY_HALVES, W4A16_ROTARY_NEIGHBOURS
+
+
+def w4a16_rotary(q, k, pos, axis, freq, qo, ko, tokens, q_heads, kv_heads, head, rot, axes, ldpos,
+                 ldq, ldk, ldqo, ldko, pairs=ROTARY_HALVES, dtype=DT_F16, stream=None):
+    _check("w4a16_rotary", _lib.w4a16_rotary(
+        _ptr(q), _ptr(k), _ptr(pos), _ptr(axis), _ptr(freq), _ptr(qo), _ptr(ko), tokens, q_heads,
+        kv_heads, head, rot, axes, ldpos, ldq, ldk, ldqo, ldko, pairs, dtype, _stream(stream)))
 
 
 # ---- calibration kernels ---------------------------------------------------------

@@ -953,49 +953,53 @@ int w4a16_kv4_gather(const void* cache, const int32_t* rows, const int32_t* lens
 
 namespace {
 bool kv4_attend_shape_ok(int batch, int tokens, int max_new, int max_len, int q_heads,
-                         int kv_heads, int head, int window) {
+                         int kv_heads, int head, int window, bool tree) {
   if (batch < 1 || batch > 65535 || tokens < 1 || max_new < 1 || max_new > tokens || max_len < 1 ||
       max_len > (1 << 30) || kv_heads < 1 || q_heads < kv_heads || q_heads > 65535 ||
       q_heads % kv_heads != 0 || (head != 64 && head != 128) || window < 0)
     return false;
   if ((long long)max_new * (q_heads / kv_heads) > (1LL << 30)) return false;
   const Kv4AttendPlan p =
-      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
+      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window, tree);
   return (long long)p.col_tiles <= (1LL << 30) / kv_heads / batch &&
          p.counters * sizeof(int) <= W4A16_WS_COUNTER_BYTES;
 }
-}  // namespace
 
-size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len, int q_heads,
-                                 int kv_heads, int head, int window) {
-  if (!kv4_attend_shape_ok(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window))
+size_t kv4_workspace(int batch, int tokens, int max_new, int max_len, int q_heads, int kv_heads,
+                     int head, int window, bool tree) {
+  if (!kv4_attend_shape_ok(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window, tree))
     return 0;
   const Kv4AttendPlan p =
-      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
+      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window, tree);
   return (p.counters + 63) / 64 * 64 * sizeof(int) + p.floats * sizeof(float);
 }
 
-int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
-                        const int32_t* table, const void* cache, uint16_t* out, float* lse,
-                        int batch, int tokens, int max_new, int max_len, int ldq, int ldo,
-                        int q_heads, int kv_heads, int head, int group, int page, int pages,
-                        int width, int window, float scale, int dtype, void* stream) {
+// Attention of new tokens in a row (mask NULL) or of trees.
+int kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
+                  const int32_t* table, const void* cache, const uint32_t* mask,
+                  const int32_t* depth, uint16_t* out, float* lse, int batch, int tokens,
+                  int max_new, int max_len, int words, int ldq, int ldo, int q_heads, int kv_heads,
+                  int head, int group, int page, int pages, int width, int window, float scale,
+                  int dtype, void* stream) {
+  const bool tree = mask != nullptr;
   const void* const p16[] = {q, cache, out};
   const int32_t* const p4[] = {rows, lens, table};
   int rc = check_kv4(p16, 3, p4, batch, tokens, max_new, kv_heads, head, group, page, pages, width,
                      dtype);
   if (rc) return rc;
-  if (!kv4_attend_shape_ok(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window) ||
+  if (!kv4_attend_shape_ok(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window,
+                           tree) ||
       !row_stride_ok(ldq, (long long)q_heads * head) ||
-      !row_stride_ok(ldo, (long long)q_heads * head))
+      !row_stride_ok(ldo, (long long)q_heads * head) ||
+      (tree && (words < 1 || 32LL * words < max_new)))
     return W4A16_ERR_SHAPE;
   if (!(scale > 0.f)) return W4A16_ERR_ARG;
-  if (!aligned4(lse)) return W4A16_ERR_ALIGN;
+  if (!aligned4(lse) || !aligned4(mask) || !aligned4(depth)) return W4A16_ERR_ALIGN;
   int dev;
   if ((rc = check_device(&dev))) return rc;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Kv4AttendPlan plan =
-      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window);
+      kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window, tree);
   int* cnt;
   float* part;
   if ((rc = get_workspace(dev, st, plan.counters, plan.floats, &cnt, &part, KV4_STRIPES,
@@ -1024,8 +1028,163 @@ int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* l
   a.width = width;
   a.window = window < (1 << 30) ? window : 1 << 30;  // no cached token lies further back
   a.scale = scale;
+  a.mask = mask;
+  a.depth = depth;
+  a.words = words;
   return launched(
       launch_kv4_attend(plan, a, head, head / group, dtype == W4A16_DT_BF16, st));
+}
+
+// What fork and compact share beside check_kv4 (layers of a pool, `stride` bytes apart).
+bool kv4_layers_ok(int layers, size_t stride, int kv_heads, int head, int group, int page,
+                   int pages) {
+  return layers >= 1 && (long long)layers * kv_heads <= KV4_LAYER_HEADS && stride % 16 == 0 &&
+         stride <= ((size_t)1 << 46) &&
+         (layers == 1 || stride >= (size_t)pages * w4a16_kv4_page_bytes(kv_heads, head, group, page));
+}
+}  // namespace
+
+size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len, int q_heads,
+                                 int kv_heads, int head, int window) {
+  return kv4_workspace(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window, false);
+}
+
+int w4a16_kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
+                        const int32_t* table, const void* cache, uint16_t* out, float* lse,
+                        int batch, int tokens, int max_new, int max_len, int ldq, int ldo,
+                        int q_heads, int kv_heads, int head, int group, int page, int pages,
+                        int width, int window, float scale, int dtype, void* stream) {
+  return kv4_attention(q, rows, lens, table, cache, nullptr, nullptr, out, lse, batch, tokens,
+                       max_new, max_len, 0, ldq, ldo, q_heads, kv_heads, head, group, page, pages,
+                       width, window, scale, dtype, stream);
+}
+
+// ---- trees of drafted tokens ---------------------------------------------------------------
+int w4a16_kv4_tree(const int32_t* parent, const int32_t* rows, const int32_t* lens, uint32_t* mask,
+                   int32_t* depth, int32_t* pos, int batch, int tokens, int max_new, int words,
+                   int window, void* stream) {
+  if (!parent || !rows || !lens || !mask) return W4A16_ERR_NULL;
+  if (batch < 1 || batch > 65535 || tokens < 1 || max_new < 1 || max_new > tokens ||
+      max_new > KV4_TREE_NODES || words < 1 || 32LL * words < max_new || window < 0)
+    return W4A16_ERR_SHAPE;
+  if (!aligned4(parent) || !aligned4(rows) || !aligned4(lens) || !aligned4(mask) ||
+      !aligned4(depth) || !aligned4(pos))
+    return W4A16_ERR_ALIGN;
+  int rc = check_device(nullptr);
+  if (rc) return rc;
+  const Kv4TreeArgs a{parent, rows, lens, mask, depth, pos, batch, tokens, max_new, words,
+                      window > 0 ? window : KV4_TREE_NODES};
+  return launched(launch_kv4_tree(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t w4a16_kv4_tree_workspace_bytes(int batch, int tokens, int max_new, int max_len, int q_heads,
+                                      int kv_heads, int head, int window) {
+  return kv4_workspace(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window, true);
+}
+
+int w4a16_kv4_tree_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
+                             const int32_t* table, const void* cache, const uint32_t* mask,
+                             const int32_t* depth, uint16_t* out, float* lse, int batch,
+                             int tokens, int max_new, int max_len, int words, int ldq, int ldo,
+                             int q_heads, int kv_heads, int head, int group, int page, int pages,
+                             int width, int window, float scale, int dtype, void* stream) {
+  if (!mask || (window > 0 && !depth)) return W4A16_ERR_NULL;
+  return kv4_attention(q, rows, lens, table, cache, mask, depth, out, lse, batch, tokens, max_new,
+                       max_len, words, ldq, ldo, q_heads, kv_heads, head, group, page, pages,
+                       width, window, scale, dtype, stream);
+}
+
+int w4a16_kv4_compact(void* cache, const int32_t* path, const int32_t* count, const int32_t* rows,
+                      const int32_t* lens, const int32_t* table, int32_t* lens_out, int batch,
+                      int tokens, int max_new, int max_path, int layers, size_t layer_bytes,
+                      int kv_heads, int head, int group, int page, int pages, int width,
+                      void* stream) {
+  if (!path || !count || !lens_out) return W4A16_ERR_NULL;
+  const void* const p16[] = {cache};
+  const int32_t* const p4[] = {rows, lens, table};
+  int rc = check_kv4(p16, 1, p4, batch, tokens, max_new, kv_heads, head, group, page, pages, width,
+                     W4A16_DT_F16);
+  if (rc) return rc;
+  if (max_path < 1 || !kv4_layers_ok(layers, layer_bytes, kv_heads, head, group, page, pages))
+    return W4A16_ERR_SHAPE;
+  if (lens_out == lens) return W4A16_ERR_ARG;
+  if (!aligned4(path) || !aligned4(count) || !aligned4(lens_out)) return W4A16_ERR_ALIGN;
+  if ((rc = check_device(nullptr))) return rc;
+  const Kv4CompactArgs a{static_cast<char*>(cache), path, count, rows, lens, table, lens_out, batch,
+                         tokens, max_new, max_path, layers, kv_heads, page, pages, width,
+                         layer_bytes};
+  return launched(launch_kv4_compact(a, head, head / group, static_cast<hipStream_t>(stream)));
+}
+
+int w4a16_kv4_fork(void* cache, const int32_t* table, const int32_t* lens, const int32_t* parent,
+                   const int32_t* keep, const int32_t* room, const uint8_t* pinned,
+                   int32_t* table_out, int32_t* lens_out, int32_t* missing, int batch,
+                   int batch_out, int layers, size_t layer_bytes, int kv_heads, int head, int group,
+                   int page, int pages, int width, void* stream) {
+  if (!table_out || !lens_out) return W4A16_ERR_NULL;
+  const void* const p16[] = {cache};
+  const int32_t* const p4[] = {table, lens, parent};
+  int rc = check_kv4(p16, 1, p4, batch, 1, 1, kv_heads, head, group, page, pages, width,
+                     W4A16_DT_F16);
+  if (rc) return rc;
+  if (batch_out < 1 || batch_out > KV4_FORK_ROWS || pages > KV4_FORK_PAGES ||
+      !kv4_layers_ok(layers, layer_bytes, kv_heads, head, group, page, pages))
+    return W4A16_ERR_SHAPE;
+  if (table_out == table || lens_out == lens) return W4A16_ERR_ARG;
+  if (!aligned4(keep) || !aligned4(room) || !aligned4(table_out) || !aligned4(lens_out) ||
+      !aligned4(missing))
+    return W4A16_ERR_ALIGN;
+  if ((rc = check_device(nullptr))) return rc;
+  const Kv4ForkArgs a{static_cast<char*>(cache), table, lens, parent, keep, room, pinned, table_out,
+                      lens_out, missing, batch, batch_out, layers, kv_heads, page, pages, width,
+                      layer_bytes};
+  return launched(launch_kv4_fork(a, head, head / group, static_cast<hipStream_t>(stream)));
+}
+
+// ---- rotary positions ------------------------------------------------------------------------
+int w4a16_rotary(const uint16_t* q, const uint16_t* k, const int32_t* pos, const int32_t* axis,
+                 const float* freq, uint16_t* qo, uint16_t* ko, int tokens, int q_heads,
+                 int kv_heads, int head, int rot, int axes, int ldpos, int ldq, int ldk, int ldqo,
+                 int ldko, int pairs, int dtype, void* stream) {
+  if (!q || !qo || !pos || !freq || (kv_heads > 0 && (!k || !ko)) || (axes > 1 && !axis))
+    return W4A16_ERR_NULL;
+  if (!is_dtype(dtype) || (pairs != W4A16_ROTARY_HALVES && pairs != W4A16_ROTARY_NEIGHBOURS))
+    return W4A16_ERR_ARG;
+  if (tokens < 1 || tokens > ROTARY_MAX_TOKENS || q_heads < 1 || kv_heads < 0 || head < 16 ||
+      head % 8 != 0 || head > ROTARY_MAX_HEAD || rot < 16 || rot % 16 != 0 || rot > head ||
+      ((long long)q_heads + kv_heads) * head > (1 << 24) || axes < 1 || ldpos < tokens ||
+      !row_stride_ok(ldq, (long long)q_heads * head) ||
+      !row_stride_ok(ldqo, (long long)q_heads * head) ||
+      (kv_heads > 0 && (!row_stride_ok(ldk, (long long)kv_heads * head) ||
+                        !row_stride_ok(ldko, (long long)kv_heads * head))) ||
+      (qo == q && ldqo != ldq) || (kv_heads > 0 && ko == k && ldko != ldk))
+    return W4A16_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(qo) || (kv_heads > 0 && (!aligned16(k) || !aligned16(ko))) ||
+      !aligned4(pos) || !aligned4(axis) || !aligned4(freq))
+    return W4A16_ERR_ALIGN;
+  int rc = check_device(nullptr);
+  if (rc) return rc;
+  RotaryArgs a{};
+  a.q = q;
+  a.k = k;
+  a.pos = pos;
+  a.axis = axis;
+  a.freq = freq;
+  a.qo = qo;
+  a.ko = ko;
+  a.tokens = tokens;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.head = head;
+  a.rot = rot;
+  a.axes = axes;
+  a.ldpos = ldpos;
+  a.ldq = ldq;
+  a.ldk = ldk;
+  a.ldqo = ldqo;
+  a.ldko = ldko;
+  return launched(launch_rotary(a, pairs == W4A16_ROTARY_NEIGHBOURS, dtype == W4A16_DT_BF16,
+                                static_cast<hipStream_t>(stream)));
 }
 
 // ---- calibration kernels -------------------------------------------------------------

@@ -224,6 +224,9 @@ struct Kv4AttendArgs {
   int target;         // chunks to cut all tiles' blocks into
   int chunk, chunks;  // least blocks of a chunk, most chunks of a tile
   int slots, tiles;   // workgroups and tiles that the launch has room for
+  const uint32_t* mask;  // of the nodes of trees, `words` a token; NULL: causal attention
+  const int* depth;      // of the nodes; not read without a window
+  int words;
 };
 struct Kv4AttendPlan {
   int cols;           // columns of a tile: 8, 16 (kv4_attention.hip) or 128 (kv4_prefill.hip)
@@ -234,10 +237,54 @@ constexpr int KV4_STRIPES = 512;  // most stripes of a launch, and the wide tile
 // workspace of any plan whose tiles have at most that many columns
 size_t kv4_attend_most_floats(int cols, int D);
 Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, int q_heads,
-                              int heads, int D, int window);
+                              int heads, int D, int window, bool tree);
 hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& a, int D, int groups,
                              bool bf, hipStream_t st);
 hipError_t launch_kv4_prefill(const Kv4AttendArgs& a, int D, int groups, bool bf, hipStream_t st);
+
+// kv4_tree.hip; depth and pos may be NULL, window is above 0
+constexpr int KV4_TREE_NODES = 4096;
+struct Kv4TreeArgs {
+  const int *parent, *rows, *lens;
+  uint32_t* mask;
+  int *depth, *pos;
+  int batch, tokens, max_new, words, window;
+};
+hipError_t launch_kv4_tree(const Kv4TreeArgs& a, hipStream_t st);
+
+// kv4_pages.hip; layers lie `stride` bytes apart; keep, room, pinned and missing may be NULL
+constexpr int KV4_FORK_ROWS = 2048, KV4_FORK_PAGES = 1 << 19;  // what LDS holds of them
+constexpr int KV4_LAYER_HEADS = 1 << 20;
+struct Kv4ForkArgs {
+  char* cache;
+  const int *table, *lens, *parent, *keep, *room;
+  const uint8_t* pinned;
+  int *table_out, *lens_out, *missing;
+  int batch, rows, layers, heads, page, pages, width;
+  size_t stride;
+};
+hipError_t launch_kv4_fork(const Kv4ForkArgs& a, int D, int groups, hipStream_t st);
+struct Kv4CompactArgs {
+  char* cache;
+  const int *path, *count, *rows, *lens, *table;
+  int* lens_out;
+  int batch, tokens, max_new, max_path, layers, heads, page, pages, width;
+  size_t stride;
+};
+hipError_t launch_kv4_compact(const Kv4CompactArgs& a, int D, int groups, hipStream_t st);
+
+// rotary.hip; axis may be NULL (one axis), k and ko with kv_heads 0
+constexpr int ROTARY_MAX_HEAD = 512, ROTARY_MAX_TOKENS = 1 << 25;
+struct RotaryArgs {
+  const uint16_t *q, *k;
+  const int *pos, *axis;
+  const float* freq;
+  uint16_t *qo, *ko;
+  int tokens, q_heads, kv_heads, head, rot, axes, ldpos, ldq, ldk, ldqo, ldko;
+  int items_head, items, piece;  // items of a head, of a token, of a workgroup
+  uint32_t magic;                // ceil(2^32 / items_head)
+};
+hipError_t launch_rotary(const RotaryArgs& a, bool neighbours, bool bf, hipStream_t st);
 
 // Calibration kernels (probes.hip).
 hipError_t launch_probe_read(const void* p, size_t bytes, uint32_t* out, hipStream_t st);

@@ -68,14 +68,18 @@ struct Kv4Place {
   int span;            // blocks that a tile of the sequence can see
 };
 
+// TREE: the new tokens are the nodes of a tree.  Each sees the tokens held before the tree
+// (those in the window of its position, which is as deep as it is) and the nodes that its bits
+// name, so every tile of a sequence has the same blocks.
+//
 // Blocks that a tile of TC columns of the sequence can see, at least 1.
-template <int TC>
+template <int TC, bool TREE>
 __device__ __forceinline__ int kv4_span(const Kv4AttendArgs& p, const Kv4Seq& s, int ratio) {
   int span = (s.len >> 5) + ((s.len & 31) != 0);
   const int most = p.width * (p.page / 32);
   span = span < most ? span : most;
   if (p.window > 0) {
-    const long long w = ((long long)p.window + TC / ratio + 1) / 32 + 2;
+    const long long w = ((long long)p.window + (TREE ? s.n : TC / ratio + 1)) / 32 + 2;
     span = span < w ? span : (int)w;
   }
   return span < 1 ? 1 : span;
@@ -126,7 +130,7 @@ __device__ __forceinline__ uint32_t wave_sums(uint32_t x) {
 // tile counts as `lead` = 16 blocks more than it has.  Where stripes of the least size
 // p.chunk are enough for all, every tile is rounded up to whole stripes instead, and no
 // workgroup has two.
-template <int TC>
+template <int TC, bool TREE>
 struct Kv4Stripes {
   static constexpr int kLead = 16;
   uint32_t total, stripe;
@@ -145,7 +149,7 @@ struct Kv4Stripes {
     Lane x{{0, 0, 0}, 1, 0, 0u, 0u};
     if (b < p.batch) {
       x.s = kv4_seq(p.rows, p.lens, b, p.tokens, p.max_new);
-      x.span = kv4_span<TC>(p, x.s, ratio);
+      x.span = kv4_span<TC, TREE>(p, x.s, ratio);
       x.tiles = (int)(((long long)x.s.n * ratio + TC - 1) / TC);
       // past 2^29 blocks in all a sequence's tiles count as one block each: the last
       // stripe of a tile takes what is left of it
@@ -212,7 +216,7 @@ struct Kv4Stripes {
 // differ widely, so every wave works out the same division from them: all tiles' blocks
 // together, cut into about p.target equal chunks.  Slot numbers run over (sequence, kv head,
 // tile, chunk).  `id` is a slot, or with BY_TILE the number of a tile (its chunk is then 0).
-template <int TC, bool BY_TILE>
+template <int TC, bool TREE, bool BY_TILE>
 __device__ __forceinline__ bool kv4_place_chunk(const Kv4AttendArgs& p, int id, Kv4Place& w) {
   const int lane = threadIdx.x & 63, ratio = p.q_heads / p.heads;
   Kv4Seq s{};
@@ -222,7 +226,7 @@ __device__ __forceinline__ bool kv4_place_chunk(const Kv4AttendArgs& p, int id, 
     span = 1;
     if (b < p.batch) {
       s = kv4_seq(p.rows, p.lens, b, p.tokens, p.max_new);
-      span = kv4_span<TC>(p, s, ratio);
+      span = kv4_span<TC, TREE>(p, s, ratio);
       tiles = (int)(((long long)s.n * ratio + TC - 1) / TC);
     }
   };
@@ -284,15 +288,15 @@ __device__ __forceinline__ bool kv4_place_chunk(const Kv4AttendArgs& p, int id, 
   return false;
 }
 
-// Tokens that the columns of a tile see, and the workgroup's blocks of them: blocks
+// Tokens that the columns of a tile can see, and the workgroup's blocks of them: blocks
 // [from, to) counted from the tile's first, to < 0: all that are left.
 struct Kv4Range {
   int i0, i1;          // first and last new token of the tile
   int from;            // position of the sequence's first new token
-  int lo, hi;          // tokens that any column sees
+  int lo, hi;          // tokens that any column can see
   int blk0, blk1;
 };
-template <int TC>
+template <int TC, bool TREE>
 __device__ __forceinline__ Kv4Range kv4_range(const Kv4AttendArgs& p, const Kv4Seq& s, int tile,
                                               int ratio, int from, int to) {
   Kv4Range r;
@@ -300,8 +304,8 @@ __device__ __forceinline__ Kv4Range kv4_range(const Kv4AttendArgs& p, const Kv4S
   const int end = (tile * TC + TC - 1) / ratio;
   r.i1 = end < s.n - 1 ? end : s.n - 1;
   r.from = s.len - s.n;
-  r.hi = r.from + r.i1 + 1;
-  const long long lo = p.window > 0 ? (long long)r.from + r.i0 - p.window + 1 : 0;
+  r.hi = r.from + (TREE ? s.n : r.i1 + 1);
+  const long long lo = p.window > 0 ? (long long)r.from + (TREE ? 0 : r.i0) - p.window + 1 : 0;
   r.lo = lo < 0 ? 0 : (int)lo;
   const int most = p.width * (p.page / 32);
   int stop = r.hi <= 0 ? 0 : (r.hi >> 5) + ((r.hi & 31) != 0);
@@ -309,6 +313,41 @@ __device__ __forceinline__ Kv4Range kv4_range(const Kv4AttendArgs& p, const Kv4S
   r.blk0 = r.lo / 32 + from;
   r.blk1 = to < 0 || r.lo / 32 + to > stop ? stop : r.lo / 32 + to;
   return r;
+}
+
+// TREE: the first token that node `row` of the sequence sees of those before the tree (their
+// number is `from`; node r.from + j of the cache is node j).
+__device__ __forceinline__ int kv4_tree_first(const Kv4AttendArgs& p, const Kv4Seq& s, int row) {
+  if (p.window <= 0) return 0;
+  int d = p.depth[row];
+  d = d < 0 ? 0 : d > s.n - 1 ? s.n - 1 : d;
+  const long long first = (long long)(s.len - s.n) + d - p.window + 1;
+  return first < 0 ? 0 : (int)first;
+}
+// TREE: which of the 32 tokens from t0 on node `row` sees, a bit each.
+__device__ __forceinline__ uint32_t kv4_tree_sees(const Kv4AttendArgs& p, const Kv4Seq& s, int row,
+                                                  int first, int t0) {
+  const int rel = t0 - (s.len - s.n);  // the node at t0
+  uint32_t sees = 0;
+  if (rel < 0) {
+    sees = rel <= -32 ? 0xFFFFFFFFu : (1u << -rel) - 1u;
+    if (first > t0) sees = first - t0 >= 32 ? 0u : sees & (0xFFFFFFFFu << (first - t0));
+  }
+  if (rel > -32) {
+    const uint32_t* bits = p.mask + (size_t)row * p.words;
+    uint32_t nodes;
+    if (rel < 0) {
+      nodes = bits[0] << -rel;
+    } else {
+      const int at = rel >> 5;
+      const uint32_t a = at < p.words ? bits[at] : 0u;
+      const uint32_t b = at + 1 < p.words ? bits[at + 1] : 0u;
+      nodes = (uint32_t)(((uint64_t)b << 32 | a) >> (rel & 31));
+    }
+    const int left = s.n - rel;  // nodes from t0 on
+    sees |= left >= 32 ? nodes : left <= 0 ? 0u : nodes & ((1u << left) - 1u);
+  }
+  return sees;
 }
 
 }  // namespace w4a16

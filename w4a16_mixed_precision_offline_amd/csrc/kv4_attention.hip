@@ -109,7 +109,7 @@ __device__ __forceinline__ uint32_t swap8(uint32_t x) {
 // of the matrix instructions serve the same columns again: K q^T leaves tile 0's tokens in
 // lanes r < 8 and tile 1's in the others, so each logit is worked on once, and V^T p^T
 // takes p's upper part from lanes r < 8 and its lower part (fp16 rows) from the others.
-template <int D, int NG, int TC, bool BF>
+template <int D, int NG, int TC, bool BF, bool TREE>
 __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p) {
   constexpr int J = D / 32, JG = J / NG, NT = D / 16;
   constexpr int E = TC / 2;       // logits of a lane in a block
@@ -120,8 +120,8 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int r = lane & 15, g = lane >> 4;
   const int ratio = p.q_heads / p.heads;
-  Kv4Stripes<TC> stripes;
-  typename Kv4Stripes<TC>::Lane lanes;
+  Kv4Stripes<TC, TREE> stripes;
+  typename Kv4Stripes<TC, TREE>::Lane lanes;
   uint32_t pos = 0, stop = 1;
   if (p.slots) {
     lanes = stripes.init(p, ratio);
@@ -151,7 +151,8 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
     tile = w.tile;
     pos = 1;
   }
-  const Kv4Range rg = kv4_range<TC>(p, seq, tile, ratio, r0, r1 == (uint32_t)span ? -1 : (int)r1);
+  const Kv4Range rg =
+      kv4_range<TC, TREE>(p, seq, tile, ratio, r0, r1 == (uint32_t)span ? -1 : (int)r1);
   if (rg.i0 >= seq.n) return;  // a tile past the sequence's last, in a launch without stripes
   const int rc = TC == 8 ? r & 7 : r;
   const int col = tile * TC + rc, ci = col / ratio;
@@ -160,10 +161,11 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
   const int row = seq.first + (live ? ci : 0);
   // tokens seen: column [first, last], any column [lo, hi), every column [all_lo, all_hi)
   const int lo = rg.lo, hi = rg.hi;
+  // (TREE: those before the tree; its own blocks always take the masked path)
   const int last = live ? rg.from + ci : -1;
-  const int first = p.window > 0 ? last - p.window + 1 : 0;
-  const int all_hi = rg.from + rg.i0 + 1;
-  const int all_lo = p.window > 0 ? rg.from + rg.i1 - p.window + 1 : 0;
+  const int first = TREE ? kv4_tree_first(p, seq, row) : p.window > 0 ? last - p.window + 1 : 0;
+  const int all_hi = TREE ? rg.from : rg.from + rg.i0 + 1;
+  const int all_lo = p.window > 0 ? rg.from + (TREE ? seq.n - 1 : rg.i1) - p.window + 1 : 0;
 
   const int page_blocks = p.page / 32;
   const size_t page_bytes = (size_t)p.heads * page_blocks * kv4_block_bytes(D, NG);
@@ -293,15 +295,21 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
       for (int e = 0; e < E; ++e) x[e] *= more;
     }
     if (t0 < all_lo || t0 + 32 > all_hi) {
+      uint32_t sees = 0, any = 0;  // TREE: tokens that the column, that any column sees
+      if constexpr (TREE) {
+        sees = any = live ? kv4_tree_sees(p, seq, row, first, t0) : 0u;
+#pragma unroll
+        for (int off = 1; off < TC; off <<= 1) any |= (uint32_t)__shfl_xor((int)any, off);
+      }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int pos = t0 + (TC == 8 ? 4 * g + e + 2 * (r & 8) : kv4_slot_token(g, e));
-        if (pos < first || pos > last) x[e] = -INFINITY;
+        const int t = TC == 8 ? 4 * g + e + 2 * (r & 8) : kv4_slot_token(g, e);
+        if (TREE ? (sees >> t & 1u) == 0 : t0 + t < first || t0 + t > last) x[e] = -INFINITY;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int pos = t0 + kv4_slot_token(g, e);
-        if (pos < lo || pos >= hi) {
+        const int t = kv4_slot_token(g, e);
+        if (TREE ? (any >> t & 1u) == 0 : t0 + t < lo || t0 + t >= hi) {
 #pragma unroll
           for (int q = 0; q < NG; ++q) {
             const uint32_t keep = e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
@@ -539,13 +547,20 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
 }
 
 typedef void (*AttendFn)(Kv4AttendArgs);
-template <int TC, bool BF>
+template <int TC, bool BF, bool TREE>
 AttendFn attend_kernel(int D, int groups) {
   if (D == 128)
-    return groups == 1 ? kv4_attend_kernel<128, 1, TC, BF>
-                       : groups == 2 ? kv4_attend_kernel<128, 2, TC, BF>
-                                     : kv4_attend_kernel<128, 4, TC, BF>;
-  return groups == 1 ? kv4_attend_kernel<64, 1, TC, BF> : kv4_attend_kernel<64, 2, TC, BF>;
+    return groups == 1 ? kv4_attend_kernel<128, 1, TC, BF, TREE>
+                       : groups == 2 ? kv4_attend_kernel<128, 2, TC, BF, TREE>
+                                     : kv4_attend_kernel<128, 4, TC, BF, TREE>;
+  return groups == 1 ? kv4_attend_kernel<64, 1, TC, BF, TREE>
+                     : kv4_attend_kernel<64, 2, TC, BF, TREE>;
+}
+template <bool TREE>
+AttendFn attend_kernel(int cols, bool bf, int D, int groups) {
+  if (cols == 8)
+    return bf ? attend_kernel<8, true, TREE>(D, groups) : attend_kernel<8, false, TREE>(D, groups);
+  return bf ? attend_kernel<16, true, TREE>(D, groups) : attend_kernel<16, false, TREE>(D, groups);
 }
 
 }  // namespace
@@ -556,7 +571,7 @@ size_t kv4_attend_most_floats(int cols, int D) {
 }
 
 Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, int q_heads,
-                              int heads, int D, int window) {
+                              int heads, int D, int window, bool tree) {
   Kv4AttendPlan p{};
   const int ratio = q_heads / heads;
   const long long columns = (long long)max_new * ratio;
@@ -568,8 +583,8 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
   tiles *= heads;
   // blocks a tile can see: the window of its first token up to its last
   long long span = ((long long)max_len + 31) / 32;
-  if (window > 0 && span > ((long long)window + p.cols / ratio + 1) / 32 + 2)
-    span = ((long long)window + p.cols / ratio + 1) / 32 + 2;
+  const long long near = ((long long)window + (tree ? max_new : p.cols / ratio + 1)) / 32 + 2;
+  if (window > 0 && span > near) span = near;
   if (p.cols == 128) {
     // Chunks of 8 / 16 / 32 blocks at least, us: 32 new tokens of 8 sequences on 2 kv heads, to
     // 16384: 55 / 47 / 56; 200 on 4, 2000: 33 / 35 / 49; 64 of 4 on 8, to 4096: 65 / 65 / 60;
@@ -616,10 +631,8 @@ hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& arg
   if (plan.cols == 128) return launch_kv4_prefill(a, D, groups, bf, st);
   const long long units = ((long long)a.heads * a.batch + 7) / 8 * 8;
   const unsigned grid = plan.slots ? plan.target : (unsigned)(units * plan.col_tiles);
-  const AttendFn fn = plan.cols == 8
-                          ? (bf ? attend_kernel<8, true>(D, groups) : attend_kernel<8, false>(D, groups))
-                          : (bf ? attend_kernel<16, true>(D, groups)
-                                : attend_kernel<16, false>(D, groups));
+  const AttendFn fn = a.mask ? attend_kernel<true>(plan.cols, bf, D, groups)
+                             : attend_kernel<false>(plan.cols, bf, D, groups);
   hipLaunchKernelGGL(fn, kv4_grid(grid), dim3(64 * AW), 0, st, a);
   return hipGetLastError();
 }

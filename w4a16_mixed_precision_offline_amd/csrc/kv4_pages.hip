@@ -1,0 +1,410 @@
+// Pages of the 4-bit cache: which sequence has which (fork), and tokens moved inside a
+// sequence (compact).  Both serve all layers of a model in one call, `stride` bytes apart.
+#include "kv4.h"
+
+namespace w4a16 {
+
+namespace {
+
+// ---- fork ----------------------------------------------------------------------------------
+// One workgroup decides about the pages (a bit for each in LDS); nothing depends on the order in
+// which its threads come along: bits are set, and of several rows the lowest number is kept.
+constexpr int FT = 1024;  // its threads
+
+// A row of the new table: the old row and what it keeps of it.
+struct ForkRow {
+  int old, keep, whole, part, entries;  // entries: of the new row that have a page
+};
+__device__ __forceinline__ ForkRow fork_row(const Kv4ForkArgs& p, int r) {
+  ForkRow x;
+  x.old = p.parent[r];
+  const int most = p.width * p.page;
+  x.keep = 0;
+  if (x.old >= 0 && x.old < p.batch) {
+    const int len = p.lens[x.old];
+    x.keep = p.keep ? p.keep[r] : len;
+    x.keep = x.keep < len ? x.keep : len;
+    x.keep = x.keep < 0 ? 0 : x.keep < most ? x.keep : most;
+  } else {
+    x.old = 0;
+  }
+  int room = p.room ? p.room[r] : 0;
+  room = room < x.keep ? x.keep : room < most ? room : most;
+  x.whole = x.keep / p.page;
+  x.part = x.keep % p.page != 0;
+  x.entries = room / p.page + (room % p.page != 0);
+  return x;
+}
+__device__ __forceinline__ int fork_entry(const Kv4ForkArgs& p, int row, int at) {
+  const int page = p.table[(size_t)row * p.width + at];
+  return page >= 0 && page < p.pages ? page : -1;
+}
+
+__device__ __forceinline__ uint32_t slot_of(int page, uint32_t slots) {
+  return ((uint32_t)page * 2654435761u >> 12) & (slots - 1);
+}
+
+// Sums of x over the threads before each one, and over all.
+__device__ __forceinline__ int sums_before(int x, int* part, int& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int upto = x;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(upto, off);
+    if (lane >= off) upto += y;
+  }
+  if (lane == 63) part[wave] = upto;
+  __syncthreads();
+  int before = 0;
+  all = 0;
+  for (int i = 0; i < FT / 64; ++i) {
+    if (i < wave) before += part[i];
+    all += part[i];
+  }
+  __syncthreads();
+  return before + upto - x;
+}
+
+__global__ __launch_bounds__(FT) void kv4_fork_kernel(Kv4ForkArgs p, int slots) {
+  extern __shared__ int lds[];
+  const int words = (p.pages + 31) / 32, per = (words + FT - 1) / FT;
+  uint32_t* taken = reinterpret_cast<uint32_t*>(lds);  // [words]: a page is held or pinned
+  int* key = lds + words;       // [slots]: a page that rows want to go on in
+  int* low = key + slots;       // [slots]: the lowest of them
+  int* old = low + slots;       // [rows]
+  int* whole = old + p.rows;    // [rows]; then the first entry that gets a new page
+  int* start = whole + p.rows;  // [rows]: pages given to the rows before
+  int* free_upto = start + p.rows;  // [FT]: free pages in the words of the threads before
+  __shared__ int part[FT / 64];
+  const int tid = threadIdx.x;
+
+  for (int w = tid; w < words; w += FT) {
+    uint32_t bits = 0;
+    const int n = p.pages - 32 * w < 32 ? p.pages - 32 * w : 32;
+    if (n < 32) bits = 0xFFFFFFFFu << n;
+    if (p.pinned)
+      for (int i = 0; i < n; ++i) bits |= (uint32_t)(p.pinned[32 * w + i] != 0) << i;
+    taken[w] = bits;
+  }
+  for (int i = tid; i < slots; i += FT) {
+    key[i] = -1;
+    low[i] = p.rows;
+  }
+  __syncthreads();
+  for (int r = tid; r < p.rows; r += FT) {
+    const ForkRow x = fork_row(p, r);
+    p.lens_out[r] = x.keep;
+    old[r] = x.old;
+    whole[r] = x.whole;
+    const int page = x.part ? fork_entry(p, x.old, x.whole) : -1;
+    if (page < 0) continue;
+    // twice as many slots as rows: there is always a free one
+    for (uint32_t i = slot_of(page, slots);; i = (i + 1) & (slots - 1)) {
+      const int was = atomicCAS(key + i, -1, page);
+      if (was == -1 || was == page) {
+        atomicMin(low + i, r);
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  {
+    // pages held whole: as many threads to a row as there are
+    int wide = FT;
+    while (wide > 64 && wide * p.rows > FT) wide >>= 1;
+    for (int r = tid / wide; r < p.rows; r += FT / wide) {
+      const int n = whole[r], row = old[r];
+#pragma unroll 4
+      for (int i = tid % wide; i < n; i += wide) {
+        const int page = fork_entry(p, row, i);
+        if (page >= 0) atomicOr(taken + (page >> 5), 1u << (page & 31));
+      }
+    }
+  }
+  __syncthreads();
+  // who goes on in its last page, and how many pages each row is given
+  int mine[2] = {0, 0};
+  for (int r = tid, k = 0; r < p.rows; r += FT, ++k) {
+    const ForkRow x = fork_row(p, r);
+    int given = x.entries - x.whole - x.part, at = x.whole + x.part;
+    if (x.part) {
+      const int page = fork_entry(p, x.old, x.whole);
+      int kept = page;
+      if (page >= 0) {
+        uint32_t i = slot_of(page, slots);
+        while (key[i] != page) i = (i + 1) & (slots - 1);
+        // read before it is set for this row itself; the others of this page find low other
+        if (low[i] != r || (taken[page >> 5] >> (page & 31) & 1u) != 0) {
+          ++given;
+          at = x.whole;
+        } else {
+          atomicOr(taken + (page >> 5), 1u << (page & 31));
+        }
+      }
+      if (at != x.whole) p.table_out[(size_t)r * p.width + x.whole] = kept;
+    }
+    whole[r] = at;
+    mine[k] = given;
+  }
+  __syncthreads();
+  int need = 0, upto = 0;
+  for (int k = 0; k * FT < p.rows; ++k) {
+    int all;
+    const int before = sums_before(mine[k], part, all);
+    if (k * FT + tid < p.rows) start[k * FT + tid] = upto + before;
+    upto += all;
+  }
+  need = upto;
+  int spare;
+  {
+    int n = 0;
+    for (int w = tid * per; w < (tid + 1) * per && w < words; ++w) n += 32 - __popc(taken[w]);
+    free_upto[tid] = sums_before(n, part, spare);
+  }
+  if (tid == 0 && p.missing) *p.missing = need > spare ? need - spare : 0;
+  __syncthreads();
+  for (int k = tid; k < need; k += FT) {
+    int r = 0;  // the last row that starts at or before k
+    for (int lo = 0, hi = p.rows; lo < hi;) {
+      const int mid = (lo + hi) / 2;
+      if (start[mid] <= k) {
+        r = mid;
+        lo = mid + 1;
+      } else {
+        hi = mid;
+      }
+    }
+    int page = -1;
+    if (k < spare) {
+      int t = 0;
+      for (int lo = 0, hi = FT; lo < hi;) {
+        const int mid = (lo + hi) / 2;
+        if (free_upto[mid] <= k) {
+          t = mid;
+          lo = mid + 1;
+        } else {
+          hi = mid;
+        }
+      }
+      int left = k - free_upto[t], w = t * per;
+      uint32_t bits = ~taken[w];
+      while (left >= __popc(bits)) {
+        left -= __popc(bits);
+        bits = ~taken[++w];
+      }
+      for (; left > 0; --left) bits &= bits - 1;
+      page = 32 * w + __builtin_ctz(bits);
+    }
+    p.table_out[(size_t)r * p.width + whole[r] + k - start[r]] = page;
+  }
+}
+
+// What is left of the new table, and the copies of last pages: blocks that have something in
+// them.  Grid: (waves / 4 that share a layer's heads, groups of `group` <= 64 rows).
+template <int D, int NG>
+__global__ __launch_bounds__(256) void kv4_fork_copy_kernel(Kv4ForkArgs p, int group) {
+  const int r0 = blockIdx.y * group;
+  const int rows = p.rows - r0 < group ? p.rows - r0 : group;
+  const unsigned all = (unsigned)rows * p.width;
+  for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < all; i += gridDim.x * 256) {
+    const int r = r0 + (int)(i / p.width), at = i % p.width;
+    const ForkRow x = fork_row(p, r);
+    if (at < x.whole) p.table_out[(size_t)r * p.width + at] = fork_entry(p, x.old, at);
+    else if (at >= x.entries) p.table_out[(size_t)r * p.width + at] = -1;
+  }
+  const int lane = threadIdx.x & 63;
+  const int unit = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  if (unit >= p.layers * p.heads) return;
+  const int page_blocks = p.page / 32;
+  const size_t head_bytes = (size_t)page_blocks * kv4_block_bytes(D, NG);
+  char* base = p.cache + (size_t)(unit / p.heads) * p.stride + (size_t)(unit % p.heads) * head_bytes;
+  int from = -1, to = -1, size = 0;
+  if (lane < rows) {
+    const ForkRow x = fork_row(p, r0 + lane);
+    if (x.part) {
+      from = fork_entry(p, x.old, x.whole);
+      to = p.table_out[(size_t)(r0 + lane) * p.width + x.whole];
+      size = (x.keep % p.page + 31) / 32 * kv4_block_bytes(D, NG);
+    }
+  }
+  for (uint64_t go = __ballot(from >= 0 && to >= 0 && to != from); go; go &= go - 1) {
+    const int l = __builtin_ctzll(go);
+    const u32x4v* src = reinterpret_cast<const u32x4v*>(
+        base + (size_t)__builtin_amdgcn_readlane(from, l) * p.heads * head_bytes);
+    u32x4v* dst = reinterpret_cast<u32x4v*>(
+        base + (size_t)__builtin_amdgcn_readlane(to, l) * p.heads * head_bytes);
+    const int n = __builtin_amdgcn_readlane(size, l) / 16;
+#pragma unroll 4
+    for (int i = lane; i < n; i += 64) dst[i] = src[i];
+  }
+}
+
+// ---- compact -------------------------------------------------------------------------------
+// A wave serves the accepted nodes of one sequence in one layer and kv head, eight at a time.
+// Node path[j] goes to place j <= path[j], so what a later node brings has not been written
+// over by an earlier one, and within eight all is read before any of it is written.  Of K a lane
+// has one of a node's four runs of words; of V it has one or two channels, whose nibbles lie in
+// words with other tokens': it reads the (at most three) words that eight places in a row lie
+// in, and no other lane writes those.
+template <int D, int NG>
+__global__ __launch_bounds__(256) void kv4_compact_kernel(Kv4CompactArgs p, int waves) {
+  constexpr int W = D / 32;  // words of a run of K
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+  const int b = blockIdx.y;
+  const Kv4Seq s = kv4_seq(p.rows, p.lens, b, p.tokens, p.max_new);
+  int count = p.count[b];
+  count = count < 0 ? 0 : count;
+  count = count < p.max_path ? count : p.max_path;
+  count = count < s.n ? count : s.n;
+  const int from = s.len - s.n;
+  if (wave == 0 && lane == 0) p.lens_out[b] = from + count > 0 ? from + count : 0;
+  const int page_blocks = p.page / 32;
+  const size_t head_bytes = (size_t)page_blocks * kv4_block_bytes(D, NG);
+  for (int j0 = 0; j0 < count; j0 += 8) {
+    // lane j < 8: where node path[j0 + j] lies and where it goes
+    const int j = j0 + (lane & 7);
+    int node = j;
+    if (j < count) node = p.path[(size_t)b * p.max_path + j];
+    bool go = j < count && node > j && node < s.n && from + j >= 0;
+    int src_page = -1, dst_page = -1;
+    const int src = from + node, dst = from + j;
+    if (go) {
+      src_page = kv4_page(p.table, b, src >> 5, page_blocks, p.width, p.pages);
+      dst_page = kv4_page(p.table, b, dst >> 5, page_blocks, p.width, p.pages);
+    }
+    go = go && src_page >= 0 && dst_page >= 0;
+    const uint32_t goes = (uint32_t)__ballot(go) & 0xFFu;
+    if (goes == 0) continue;
+    const int src_off = (src >> 5) % page_blocks, dst_off = (dst >> 5) % page_blocks;
+    for (int unit = wave; unit < p.layers * p.heads; unit += waves) {
+      char* base = p.cache + (size_t)(unit / p.heads) * p.stride +
+                   (size_t)(unit % p.heads) * head_bytes;
+      auto block = [&](int page, int off, int l) {
+        return base + (size_t)__builtin_amdgcn_readlane(page, l) * p.heads * head_bytes +
+               (size_t)__builtin_amdgcn_readlane(off, l) * kv4_block_bytes(D, NG);
+      };
+      // K: lane 4 i + g has run g of token i; parameters: lane 8 i + .. has some of token i
+      typedef uint32_t run __attribute__((ext_vector_type(W)));
+      auto at_lane = [&](int x, int l) { return __shfl(x, l); };
+      const int ki = (lane >> 2) & 7, kg = lane & 3;
+      const bool kgo = lane < 32 && (goes >> ki & 1u) != 0;
+      const int ksp = at_lane(src_page, ki), kso = at_lane(src_off, ki), kst = at_lane(src, ki) & 31;
+      const int kdp = at_lane(dst_page, ki), kdo = at_lane(dst_off, ki), kdt = at_lane(dst, ki) & 31;
+      auto k_run = [&](int page, int off, int t) {
+        return reinterpret_cast<run*>(base + (size_t)page * p.heads * head_bytes +
+                                      (size_t)off * kv4_block_bytes(D, NG) +
+                                      (((t >> 4) * 64 + 16 * kg + (t & 15)) * W) * 4);
+      };
+      run kw;
+      if (kgo) kw = *k_run(ksp, kso, kst);
+      const int pi = lane >> 3;
+      const bool pgo = (goes >> pi & 1u) != 0;
+      const int psp = at_lane(src_page, pi), pso = at_lane(src_off, pi), pst = at_lane(src, pi) & 31;
+      const int pdp = at_lane(dst_page, pi), pdo = at_lane(dst_off, pi), pdt = at_lane(dst, pi) & 31;
+      constexpr int NP = 4 * NG;  // K's and V's s and m of each group
+      uint16_t par[(NP + 7) / 8];
+      auto params = [&](int page, int off, int t, int i) {
+        return reinterpret_cast<uint16_t*>(base + (size_t)page * p.heads * head_bytes +
+                                           (size_t)off * kv4_block_bytes(D, NG) + 32 * D) +
+               i * 32 + kv4_token_slot(t);
+      };
+#pragma unroll
+      for (int i = 0; i < (NP + 7) / 8; ++i)
+        if (pgo && 8 * i + (lane & 7) < NP) par[i] = *params(psp, pso, pst, 8 * i + (lane & 7));
+      // V: word of channel c = 64 h + lane and lane group tg of a block
+      auto v_word = [&](char* blk, int h, int tg) {
+        return reinterpret_cast<uint32_t*>(blk + 16 * D) +
+               (h * 64 + 16 * tg + (lane & 15)) * 4 + (lane >> 4);
+      };
+      uint32_t code[D / 64][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (goes >> i & 1u) {
+          const int t = __builtin_amdgcn_readlane(src, i) & 31;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            code[h][i] = *v_word(block(src_page, src_off, i), h, (t >> 2) & 3);
+        }
+      // the words of the places: those of nodes j0 .. j0 + 7 that go into group y of four places
+      const int d0 = from + j0, skew = d0 & 3;
+      uint32_t word[D / 64][3];
+      uint32_t* at[3][D / 64];
+#pragma unroll
+      for (int y = 0; y < 3; ++y) {
+        const uint32_t in = goes & (uint32_t)((0xFULL << (4 * y)) >> skew);
+        if (in == 0) continue;
+        const int i = __builtin_ctz(in);
+        char* blk = block(dst_page, dst_off, i);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          at[y][h] = v_word(blk, h, ((d0 + i) >> 2) & 3);
+          word[h][y] = *at[y][h];
+        }
+      }
+      if (kgo) *k_run(kdp, kdo, kdt) = kw;
+#pragma unroll
+      for (int i = 0; i < (NP + 7) / 8; ++i)
+        if (pgo && 8 * i + (lane & 7) < NP) *params(pdp, pdo, pdt, 8 * i + (lane & 7)) = par[i];
+#pragma unroll
+      for (int y = 0; y < 3; ++y) {
+        const uint32_t in = goes & (uint32_t)((0xFULL << (4 * y)) >> skew);
+        if (in == 0) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if ((in >> i & 1u) == 0) continue;
+          const int ts = __builtin_amdgcn_readlane(src, i), td = d0 + i;
+          const int ss = 4 * nib_pos(((ts >> 4) & 1) * 4 + (ts & 3));
+          const int sd = 4 * nib_pos(((td >> 4) & 1) * 4 + (td & 3));
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            word[h][y] = (word[h][y] & ~(15u << sd)) | ((code[h][i] >> ss & 15u) << sd);
+        }
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) *at[y][h] = word[h][y];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv4_fork(const Kv4ForkArgs& a, int D, int groups, hipStream_t st) {
+  int slots = 64;
+  while (slots < 2 * a.rows) slots *= 2;
+  const size_t lds = ((a.pages + 31) / 32 + 2 * slots + 3 * a.rows + FT) * sizeof(int);
+  hipError_t e = hipSuccess;
+  if (lds > 65536)
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kv4_fork_kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kv4_fork_kernel, dim3(1), dim3(FT), lds, st, a, slots);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  // rows of a wave: as many as leave 4096 waves
+  const int units = a.layers * a.heads;
+  int group = (int)((long long)units * a.rows / 4096);
+  group = group < 1 ? 1 : group > 64 ? 64 : group;
+  const dim3 grid((units + 3) / 4, (a.rows + group - 1) / group);
+  auto fn = D == 128 ? (groups == 1   ? kv4_fork_copy_kernel<128, 1>
+                        : groups == 2 ? kv4_fork_copy_kernel<128, 2>
+                                      : kv4_fork_copy_kernel<128, 4>)
+                     : (groups == 1 ? kv4_fork_copy_kernel<64, 1> : kv4_fork_copy_kernel<64, 2>);
+  hipLaunchKernelGGL(fn, grid, dim3(256), 0, st, a, group);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv4_compact(const Kv4CompactArgs& a, int D, int groups, hipStream_t st) {
+  // units of a wave: as many as leave 8192 waves, 4 at most
+  const int units = a.layers * a.heads;
+  long long each = (long long)units * a.batch / 8192;
+  each = each < 1 ? 1 : each > 4 ? 4 : each;
+  const int groups4 = (int)((units + 4 * each - 1) / (4 * each));
+  auto fn = D == 128 ? (groups == 1   ? kv4_compact_kernel<128, 1>
+                        : groups == 2 ? kv4_compact_kernel<128, 2>
+                                      : kv4_compact_kernel<128, 4>)
+                     : (groups == 1 ? kv4_compact_kernel<64, 1> : kv4_compact_kernel<64, 2>);
+  hipLaunchKernelGGL(fn, dim3(groups4, a.batch), dim3(256), 0, st, a, 4 * groups4);
+  return hipGetLastError();
+}
+
+}  // namespace w4a16

@@ -88,7 +88,7 @@ struct Piece {
 };
 
 // Grid without chunks: 8 x tiles x (units / 8); with: one workgroup per chunk.
-template <int D, int NG, bool BF>
+template <int D, int NG, bool BF, bool TREE>
 __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
   constexpr int J = D / 16, JG = J / NG, CT = D / 32;
   __shared__ Stage<D, NG> lds[2];
@@ -97,26 +97,30 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
   const int c = lane & 31, h = lane >> 5;
   const int ratio = p.q_heads / p.heads;
   Kv4Place w;
-  if (!(p.slots ? kv4_place_chunk<PTC, false>(p, blockIdx.x, w) : kv4_place_whole(p, w))) return;
+  if (!(p.slots ? kv4_place_chunk<PTC, TREE, false>(p, blockIdx.x, w) : kv4_place_whole(p, w)))
+    return;
   const int size = (w.span + w.chunks - 1) / w.chunks;
-  const Kv4Range rg = kv4_range<PTC>(p, w.s, w.tile, ratio, w.chunk * size,
-                                     w.chunk == w.chunks - 1 ? -1 : (w.chunk + 1) * size);
+  const Kv4Range rg = kv4_range<PTC, TREE>(p, w.s, w.tile, ratio, w.chunk * size,
+                                           w.chunk == w.chunks - 1 ? -1 : (w.chunk + 1) * size);
   if (rg.i0 >= w.s.n) return;
   const int col = w.tile * PTC + 32 * wave + c, ci = col / ratio;
   const bool live = ci < w.s.n;
   const int qh = w.head * ratio + col % ratio;
   const int row = w.s.first + (live ? ci : 0);
   // tokens seen: column [first, last], any column [lo, hi) (of the wave: [wlo, whi)), every
-  // column of the wave [all_lo, all_hi)
+  // column of the wave [all_lo, all_hi) (TREE: of those before the tree)
   const int last = live ? rg.from + ci : -1;
-  const int first = p.window > 0 ? last - p.window + 1 : 0;
+  const int first = TREE ? kv4_tree_first(p, w.s, row) : p.window > 0 ? last - p.window + 1 : 0;
   const int w0 = (w.tile * PTC + 32 * wave) / ratio;
   const int wl = (w.tile * PTC + 32 * wave + 31) / ratio;
   const int w1 = wl < w.s.n - 1 ? wl : w.s.n - 1;
-  const int whi = w0 < w.s.n ? rg.from + w1 + 1 : 0;
-  const int wlo = p.window > 0 ? rg.from + w0 - p.window + 1 : 0;
-  const int all_hi = wl < w.s.n ? rg.from + w0 + 1 : 0;
-  const int all_lo = p.window > 0 ? rg.from + w1 - p.window + 1 : 0;
+  const int whi = w0 < w.s.n ? (TREE ? rg.hi : rg.from + w1 + 1) : 0;
+  const int wlo = TREE ? rg.lo : p.window > 0 ? rg.from + w0 - p.window + 1 : 0;
+  const int all_hi = wl < w.s.n ? (TREE ? rg.from : rg.from + w0 + 1) : 0;
+  const int all_lo = p.window > 0 ? rg.from + (TREE ? w.s.n - 1 : w1) - p.window + 1 : 0;
+
+  // TREE: from here on up to the tree every column of the tile sees a token
+  const int tile_lo = TREE && p.window > 0 ? rg.from + w.s.n - p.window : 0;
 
   half8v qf[J], qm;
   float cf;
@@ -202,11 +206,18 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
     const int t0 = blk * 32, g = lane >> 4, r = lane & 15;
     if (!valid(blk, pg)) return;  // nobody looks at it
     // what no column sees may be anything: its s and m become 0
-    if (t0 < rg.lo || t0 + 32 > rg.hi) {
+    if (TREE ? t0 < tile_lo || t0 + 32 > rg.from : t0 < rg.lo || t0 + 32 > rg.hi) {
+      uint32_t any = 0;
+      if constexpr (TREE) {
+        for (int i = rg.i0 + lane; i <= rg.i1; i += 64)
+          any |= kv4_tree_sees(p, w.s, w.s.first + i, kv4_tree_first(p, w.s, w.s.first + i), t0);
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) any |= (uint32_t)__shfl_xor((int)any, off);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int pos = t0 + kv4_slot_token(g, e);
-        if (pos < rg.lo || pos >= rg.hi) {
+        const int t = kv4_slot_token(g, e);
+        if (TREE ? (any >> t & 1u) == 0 : t0 + t < rg.lo || t0 + t >= rg.hi) {
           const uint32_t keep = e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
           for (int i = 0; i < Piece<D, NG>::GH; ++i) {
@@ -271,10 +282,12 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
       for (int t = 0; t < CT; ++t) vf[s][t] = __builtin_bit_cast(half8v, st.v[i_blk][s][t][lane]);
     __builtin_amdgcn_sched_barrier(0);
     if (t0 < all_lo || t0 + 32 > all_hi) {
+      uint32_t sees = 0;
+      if constexpr (TREE) sees = live ? kv4_tree_sees(p, w.s, row, first, t0) : 0u;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int pos = t0 + 4 * h + 8 * (i >> 2) + (i & 3);
-        if (pos < first || pos > last) x[i] = -INFINITY;
+        const int t = 4 * h + 8 * (i >> 2) + (i & 3);
+        if (TREE ? (sees >> t & 1u) == 0 : t0 + t < first || t0 + t > last) x[i] = -INFINITY;
       }
     }
     float top = x[0];
@@ -406,13 +419,13 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
 
 // Joins a tile's chunks, in their order.  Grid: (tiles, D / 8): a workgroup has 8 channels of
 // the tile's 128 columns, a thread 4 of one.
-template <int D, bool BF>
+template <int D, bool BF, bool TREE>
 __global__ __launch_bounds__(256) void kv4_prefill_join_kernel(Kv4AttendArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 31, h = lane >> 5, t = blockIdx.y >> 2, k = blockIdx.y & 3;
   const int ratio = p.q_heads / p.heads;
   Kv4Place w;
-  if (!kv4_place_chunk<PTC, true>(p, blockIdx.x, w) || w.chunks == 1) return;
+  if (!kv4_place_chunk<PTC, TREE, true>(p, blockIdx.x, w) || w.chunks == 1) return;
   const int col = w.tile * PTC + 32 * wave + c, ci = col / ratio;
   if (ci >= w.s.n) return;
   const int qh = w.head * ratio + col % ratio, row = w.s.first + ci;
@@ -439,12 +452,17 @@ __global__ __launch_bounds__(256) void kv4_prefill_join_kernel(Kv4AttendArgs p) 
 }
 
 typedef void (*PrefillFn)(Kv4AttendArgs);
-template <bool BF>
+template <bool BF, bool TREE>
 PrefillFn prefill_kernel(int D, int groups) {
   if (D == 128)
-    return groups == 1 ? kv4_prefill_kernel<128, 1, BF>
-                       : groups == 2 ? kv4_prefill_kernel<128, 2, BF> : kv4_prefill_kernel<128, 4, BF>;
-  return groups == 1 ? kv4_prefill_kernel<64, 1, BF> : kv4_prefill_kernel<64, 2, BF>;
+    return groups == 1 ? kv4_prefill_kernel<128, 1, BF, TREE>
+                       : groups == 2 ? kv4_prefill_kernel<128, 2, BF, TREE>
+                                     : kv4_prefill_kernel<128, 4, BF, TREE>;
+  return groups == 1 ? kv4_prefill_kernel<64, 1, BF, TREE> : kv4_prefill_kernel<64, 2, BF, TREE>;
+}
+template <bool BF, bool TREE>
+PrefillFn join_kernel(int D) {
+  return D == 128 ? kv4_prefill_join_kernel<128, BF, TREE> : kv4_prefill_join_kernel<64, BF, TREE>;
 }
 
 }  // namespace
@@ -452,12 +470,16 @@ PrefillFn prefill_kernel(int D, int groups) {
 hipError_t launch_kv4_prefill(const Kv4AttendArgs& a, int D, int groups, bool bf, hipStream_t st) {
   const long long units = ((long long)a.heads * a.batch + 7) / 8 * 8;
   const unsigned grid = a.slots ? a.slots : (unsigned)(units * a.col_tiles);
-  hipLaunchKernelGGL(bf ? prefill_kernel<true>(D, groups) : prefill_kernel<false>(D, groups),
-                     kv4_grid(grid), dim3(256), 0, st, a);
+  const bool tree = a.mask != nullptr;
+  const PrefillFn fn = bf ? (tree ? prefill_kernel<true, true>(D, groups)
+                                  : prefill_kernel<true, false>(D, groups))
+                          : (tree ? prefill_kernel<false, true>(D, groups)
+                                  : prefill_kernel<false, false>(D, groups));
+  hipLaunchKernelGGL(fn, kv4_grid(grid), dim3(256), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.slots == 0) return e;
-  auto join = D == 128 ? (bf ? kv4_prefill_join_kernel<128, true> : kv4_prefill_join_kernel<128, false>)
-                       : (bf ? kv4_prefill_join_kernel<64, true> : kv4_prefill_join_kernel<64, false>);
+  const PrefillFn join = bf ? (tree ? join_kernel<true, true>(D) : join_kernel<true, false>(D))
+                            : (tree ? join_kernel<false, true>(D) : join_kernel<false, false>(D));
   hipLaunchKernelGGL(join, dim3(a.tiles, D / 8), dim3(256), 0, st, a);
   return hipGetLastError();
 }
