@@ -240,6 +240,8 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
                               int heads, int D, int window, bool tree);
 hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& a, int D, int groups,
                              bool bf, hipStream_t st);
+// kv4_tree_wide.hip: tiles of 128 columns of trees, a.target stripes
+hipError_t launch_kv4_tree_wide(const Kv4AttendArgs& a, int D, int groups, bool bf, hipStream_t st);
 hipError_t launch_kv4_prefill(const Kv4AttendArgs& a, int D, int groups, bool bf, hipStream_t st);
 
 // kv4_tree.hip; depth and pos may be NULL, window is above 0

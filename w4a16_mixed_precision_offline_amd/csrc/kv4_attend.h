@@ -126,13 +126,13 @@ __device__ __forceinline__ uint32_t wave_sums(uint32_t x) {
 // every workgroup works out the same division from them: the blocks of all tiles in a row,
 // in the order (sequence, kv head, tile), cut into equal stripes, one per workgroup.  A
 // stripe's first and last tile may be shared with its neighbours.
-// To begin, join and hand over a tile costs a workgroup about 4 us, as much as 16 blocks, so a
-// tile counts as `lead` = 16 blocks more than it has.  Where stripes of the least size
+// To begin, join and hand over a tile costs a workgroup about 4 us, as much as 16 blocks (tiles of
+// 128 columns: as 4), so a tile counts as `lead` blocks more than it has.  Where stripes of the least size
 // p.chunk are enough for all, every tile is rounded up to whole stripes instead, and no
 // workgroup has two.
 template <int TC, bool TREE>
 struct Kv4Stripes {
-  static constexpr int kLead = 16;
+  static constexpr int kLead = TC == 128 ? 4 : 16;
   uint32_t total, stripe;
   int lead;
 
@@ -216,7 +216,7 @@ struct Kv4Stripes {
 // differ widely, so every wave works out the same division from them: all tiles' blocks
 // together, cut into about p.target equal chunks.  Slot numbers run over (sequence, kv head,
 // tile, chunk).  `id` is a slot, or with BY_TILE the number of a tile (its chunk is then 0).
-template <int TC, bool TREE, bool BY_TILE>
+template <int TC, bool BY_TILE>
 __device__ __forceinline__ bool kv4_place_chunk(const Kv4AttendArgs& p, int id, Kv4Place& w) {
   const int lane = threadIdx.x & 63, ratio = p.q_heads / p.heads;
   Kv4Seq s{};
@@ -226,7 +226,7 @@ __device__ __forceinline__ bool kv4_place_chunk(const Kv4AttendArgs& p, int id, 
     span = 1;
     if (b < p.batch) {
       s = kv4_seq(p.rows, p.lens, b, p.tokens, p.max_new);
-      span = kv4_span<TC, TREE>(p, s, ratio);
+      span = kv4_span<TC, false>(p, s, ratio);
       tiles = (int)(((long long)s.n * ratio + TC - 1) / TC);
     }
   };

@@ -585,7 +585,7 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
   long long span = ((long long)max_len + 31) / 32;
   const long long near = ((long long)window + (tree ? max_new : p.cols / ratio + 1)) / 32 + 2;
   if (window > 0 && span > near) span = near;
-  if (p.cols == 128) {
+  if (p.cols == 128 && !tree) {
     // Chunks of 8 / 16 / 32 blocks at least, us: 32 new tokens of 8 sequences on 2 kv heads, to
     // 16384: 55 / 47 / 56; 200 on 4, 2000: 33 / 35 / 49; 64 of 4 on 8, to 4096: 65 / 65 / 60;
     // 1024 on 1, 1024: 26 / 32 / 47; no difference above.  Chunks for 256 / 512 / 768 / 1024
@@ -607,13 +607,15 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     // on 8 kv heads 9.5 / 10.2 / 11.7 / 11.5, of 4000 13.8 / 11.6 / 11.8 / 14.8, of 16000 25.4 /
     // 25.9 / 16.5 / 16.6; six to 4000 15.9 / 15.2 / 12.5 / 15.3, to 16000 26 each; 24 to 1000
     // 16.1 / 16.1 / 16.0 / 12.5, to 16000 55 each.
-    p.chunk = 8;
+    p.chunk = p.cols == 128 ? 16 : 8;
     long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
-    if (batch > 1024 || stripes <= tiles) return p;
+    const bool wide = p.cols == 128;  // trees only: always stripes
+    if (!wide && (batch > 1024 || stripes <= tiles)) return p;
     if (stripes > KV4_STRIPES) stripes = KV4_STRIPES;
     p.target = (int)stripes;
     p.slots = 2 * (int)stripes;
-    p.counters = (size_t)stripes;
+    if (!wide) p.counters = (size_t)stripes;
+    else if (stripes == 1) p.slots = 0;  // nothing to join
   }
   p.floats = (size_t)p.slots * p.cols * (D + 2);
   return p;
@@ -628,7 +630,9 @@ hipError_t launch_kv4_attend(const Kv4AttendPlan& plan, const Kv4AttendArgs& arg
   a.chunks = plan.chunks;
   a.slots = plan.slots;
   a.tiles = plan.tiles;
-  if (plan.cols == 128) return launch_kv4_prefill(a, D, groups, bf, st);
+  if (plan.cols == 128)
+    return a.mask ? launch_kv4_tree_wide(a, D, groups, bf, st)
+                  : launch_kv4_prefill(a, D, groups, bf, st);
   const long long units = ((long long)a.heads * a.batch + 7) / 8 * 8;
   const unsigned grid = plan.slots ? plan.target : (unsigned)(units * plan.col_tiles);
   const AttendFn fn = a.mask ? attend_kernel<true>(plan.cols, bf, D, groups)

@@ -10,6 +10,7 @@ namespace {
 // One workgroup decides about the pages (a bit for each in LDS); nothing depends on the order in
 // which its threads come along: bits are set, and of several rows the lowest number is kept.
 constexpr int FT = 1024;  // its threads
+static_assert(KV4_FORK_ROWS <= 2 * FT, "a thread has two rows");
 
 // A row of the new table: the old row and what it keeps of it.
 struct ForkRow {
@@ -78,83 +79,110 @@ __global__ __launch_bounds__(FT) void kv4_fork_kernel(Kv4ForkArgs p, int slots) 
   __shared__ int part[FT / 64];
   const int tid = threadIdx.x;
 
-  for (int w = tid; w < words; w += FT) {
-    uint32_t bits = 0;
-    const int n = p.pages - 32 * w < 32 ? p.pages - 32 * w : 32;
-    if (n < 32) bits = 0xFFFFFFFFu << n;
-    if (p.pinned)
-      for (int i = 0; i < n; ++i) bits |= (uint32_t)(p.pinned[32 * w + i] != 0) << i;
-    taken[w] = bits;
+  // rows tid and tid + FT, in registers: their loads are in flight beside those of `pinned`
+  ForkRow row[2];
+  int page[2];  // the last one of which a part is kept, -1: there is none
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k * FT + tid < p.rows) row[k] = fork_row(p, k * FT + tid);
+  // a wave makes two words of 64 pages' bytes, eight times in flight
+  for (int w0 = 2 * (tid >> 6); w0 < words; w0 += 8 * 2 * (FT / 64)) {
+    bool held[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = 32 * (w0 + j * 2 * (FT / 64)) + (tid & 63);
+      held[j] = i >= p.pages || (p.pinned && p.pinned[i] != 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint64_t bits = __ballot(held[j]);
+      const int w = w0 + j * 2 * (FT / 64) + (tid & 63);
+      if ((tid & 63) < 2 && w < words) taken[w] = (uint32_t)(bits >> (32 * (tid & 63)));
+    }
   }
   for (int i = tid; i < slots; i += FT) {
     key[i] = -1;
     low[i] = p.rows;
   }
-  __syncthreads();
-  for (int r = tid; r < p.rows; r += FT) {
-    const ForkRow x = fork_row(p, r);
-    p.lens_out[r] = x.keep;
-    old[r] = x.old;
-    whole[r] = x.whole;
-    const int page = x.part ? fork_entry(p, x.old, x.whole) : -1;
-    if (page < 0) continue;
-    // twice as many slots as rows: there is always a free one
-    for (uint32_t i = slot_of(page, slots);; i = (i + 1) & (slots - 1)) {
-      const int was = atomicCAS(key + i, -1, page);
-      if (was == -1 || was == page) {
-        atomicMin(low + i, r);
-        break;
-      }
-    }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = k * FT + tid;
+    page[k] = -1;
+    if (r >= p.rows) continue;
+    p.lens_out[r] = row[k].keep;
+    old[r] = row[k].old;
+    whole[r] = row[k].whole;
+    if (row[k].part) page[k] = fork_entry(p, row[k].old, row[k].whole);
   }
   __syncthreads();
   {
-    // pages held whole: as many threads to a row as there are
+    // Pages held whole: 16 threads to a row, more where there are fewer than 64 rows, with 8
+    // entries each in flight.
     int wide = FT;
-    while (wide > 64 && wide * p.rows > FT) wide >>= 1;
+    while (wide > 16 && wide * p.rows > FT) wide >>= 1;
     for (int r = tid / wide; r < p.rows; r += FT / wide) {
-      const int n = whole[r], row = old[r];
-#pragma unroll 4
-      for (int i = tid % wide; i < n; i += wide) {
-        const int page = fork_entry(p, row, i);
-        if (page >= 0) atomicOr(taken + (page >> 5), 1u << (page & 31));
+      const int n = whole[r], from = old[r];
+      for (int i0 = tid % wide; i0 < n; i0 += 8 * wide) {
+        int x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = i0 + j * wide;
+          x[j] = p.table[(size_t)from * p.width + (i < n ? i : i0)];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (x[j] >= 0 && x[j] < p.pages) atomicOr(taken + (x[j] >> 5), 1u << (x[j] & 31));
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (page[k] < 0) continue;
+    // twice as many slots as rows: there is always a free one
+    for (uint32_t i = slot_of(page[k], slots);; i = (i + 1) & (slots - 1)) {
+      const int was = atomicCAS(key + i, -1, page[k]);
+      if (was == -1 || was == page[k]) {
+        atomicMin(low + i, k * FT + tid);
+        break;
       }
     }
   }
   __syncthreads();
   // who goes on in its last page, and how many pages each row is given
   int mine[2] = {0, 0};
-  for (int r = tid, k = 0; r < p.rows; r += FT, ++k) {
-    const ForkRow x = fork_row(p, r);
-    int given = x.entries - x.whole - x.part, at = x.whole + x.part;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = k * FT + tid;
+    if (r >= p.rows) continue;
+    const ForkRow& x = row[k];
+    mine[k] = x.entries - x.whole - x.part;
+    int at = x.whole + x.part;
     if (x.part) {
-      const int page = fork_entry(p, x.old, x.whole);
-      int kept = page;
-      if (page >= 0) {
-        uint32_t i = slot_of(page, slots);
-        while (key[i] != page) i = (i + 1) & (slots - 1);
-        // read before it is set for this row itself; the others of this page find low other
-        if (low[i] != r || (taken[page >> 5] >> (page & 31) & 1u) != 0) {
-          ++given;
+      if (page[k] >= 0) {
+        uint32_t i = slot_of(page[k], slots);
+        while (key[i] != page[k]) i = (i + 1) & (slots - 1);
+        // read before it is set for this row itself; the others of this page find `low` another
+        if (low[i] != r || (taken[page[k] >> 5] >> (page[k] & 31) & 1u) != 0) {
+          ++mine[k];
           at = x.whole;
         } else {
-          atomicOr(taken + (page >> 5), 1u << (page & 31));
+          atomicOr(taken + (page[k] >> 5), 1u << (page[k] & 31));
         }
       }
-      if (at != x.whole) p.table_out[(size_t)r * p.width + x.whole] = kept;
+      if (at != x.whole) p.table_out[(size_t)r * p.width + x.whole] = page[k];
     }
     whole[r] = at;
-    mine[k] = given;
   }
   __syncthreads();
-  int need = 0, upto = 0;
-  for (int k = 0; k * FT < p.rows; ++k) {
+  int need = 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (k * FT >= p.rows) break;
     int all;
     const int before = sums_before(mine[k], part, all);
-    if (k * FT + tid < p.rows) start[k * FT + tid] = upto + before;
-    upto += all;
+    if (k * FT + tid < p.rows) start[k * FT + tid] = need + before;
+    need += all;
   }
-  need = upto;
   int spare;
   {
     int n = 0;
@@ -200,7 +228,7 @@ __global__ __launch_bounds__(FT) void kv4_fork_kernel(Kv4ForkArgs p, int slots) 
 }
 
 // What is left of the new table, and the copies of last pages: blocks that have something in
-// them.  Grid: (waves / 4 that share a layer's heads, groups of `group` <= 64 rows).
+// them.  Grid: (waves / 4 that share the kv heads of all layers, groups of `group` <= 64 rows).
 template <int D, int NG>
 __global__ __launch_bounds__(256) void kv4_fork_copy_kernel(Kv4ForkArgs p, int group) {
   const int r0 = blockIdx.y * group;
@@ -215,9 +243,7 @@ __global__ __launch_bounds__(256) void kv4_fork_copy_kernel(Kv4ForkArgs p, int g
   const int lane = threadIdx.x & 63;
   const int unit = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
   if (unit >= p.layers * p.heads) return;
-  const int page_blocks = p.page / 32;
-  const size_t head_bytes = (size_t)page_blocks * kv4_block_bytes(D, NG);
-  char* base = p.cache + (size_t)(unit / p.heads) * p.stride + (size_t)(unit % p.heads) * head_bytes;
+  const size_t head_bytes = (size_t)(p.page / 32) * kv4_block_bytes(D, NG);
   int from = -1, to = -1, size = 0;
   if (lane < rows) {
     const ForkRow x = fork_row(p, r0 + lane);
@@ -227,6 +253,7 @@ __global__ __launch_bounds__(256) void kv4_fork_copy_kernel(Kv4ForkArgs p, int g
       size = (x.keep % p.page + 31) / 32 * kv4_block_bytes(D, NG);
     }
   }
+  char* base = p.cache + (size_t)(unit / p.heads) * p.stride + (size_t)(unit % p.heads) * head_bytes;
   for (uint64_t go = __ballot(from >= 0 && to >= 0 && to != from); go; go &= go - 1) {
     const int l = __builtin_ctzll(go);
     const u32x4v* src = reinterpret_cast<const u32x4v*>(
@@ -234,8 +261,15 @@ __global__ __launch_bounds__(256) void kv4_fork_copy_kernel(Kv4ForkArgs p, int g
     u32x4v* dst = reinterpret_cast<u32x4v*>(
         base + (size_t)__builtin_amdgcn_readlane(to, l) * p.heads * head_bytes);
     const int n = __builtin_amdgcn_readlane(size, l) / 16;
-#pragma unroll 4
-    for (int i = lane; i < n; i += 64) dst[i] = src[i];
+    for (int i0 = lane; i0 < n; i0 += 8 * 64) {  // eight loads in flight
+      u32x4v x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 64 * j < n) x[j] = src[i0 + 64 * j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 64 * j < n) dst[i0 + 64 * j] = x[j];
+    }
   }
 }
 
@@ -380,16 +414,18 @@ hipError_t launch_kv4_fork(const Kv4ForkArgs& a, int D, int groups, hipStream_t 
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kv4_fork_kernel, dim3(1), dim3(FT), lds, st, a, slots);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  // rows of a wave: as many as leave 4096 waves
+  // A wave has one layer's kv head, and one row up to 16384 waves (two for every one that the
+  // card holds at a time), more rows past that.  Four heads a wave instead, which look up once
+  // what there is to do: 24 us where one takes 20 (64 rows of which 56 copy, 32 layers of 8 heads).
   const int units = a.layers * a.heads;
-  int group = (int)((long long)units * a.rows / 4096);
+  long long group = (long long)units * a.rows / 16384;
   group = group < 1 ? 1 : group > 64 ? 64 : group;
-  const dim3 grid((units + 3) / 4, (a.rows + group - 1) / group);
+  const dim3 grid((units + 3) / 4, (unsigned)((a.rows + group - 1) / group));
   auto fn = D == 128 ? (groups == 1   ? kv4_fork_copy_kernel<128, 1>
                         : groups == 2 ? kv4_fork_copy_kernel<128, 2>
                                       : kv4_fork_copy_kernel<128, 4>)
                      : (groups == 1 ? kv4_fork_copy_kernel<64, 1> : kv4_fork_copy_kernel<64, 2>);
-  hipLaunchKernelGGL(fn, grid, dim3(256), 0, st, a, group);
+  hipLaunchKernelGGL(fn, grid, dim3(256), 0, st, a, (int)group);
   return hipGetLastError();
 }
 

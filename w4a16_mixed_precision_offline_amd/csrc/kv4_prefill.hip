@@ -29,18 +29,13 @@
 // block's product issued beside the exponentials of the block before it (with p hi + lo 640 us,
 // registers spill), two sums per product instead of one dependent chain (637 us), longest
 // sequences first (no difference).
-#include "kv4_attend.h"
+#include "kv4_wide.h"
 
 namespace w4a16 {
 
 namespace {
 
-constexpr int PTC = 128;  // columns of a workgroup
 constexpr int PS = 2;     // blocks of a stage
-
-// p's exponent is x cf - ref + 8 in one fma.  ref is some x cf rounded, so past 2^26 their
-// difference alone can lift p out of fp16: past this reference x cf is rounded first.
-constexpr float kFar = 0x1p20f;
 
 template <int D, int NG>
 struct Stage {
@@ -50,45 +45,8 @@ struct Stage {
   float s[PS][NG][32];
 };
 
-// What a thread loads of a stage: wave w serves block w / 2, half w % 2.
-template <int D, int NG>
-struct Piece {
-  static constexpr int W = D / 32;                 // words of a K or V item
-  static constexpr int GH = NG >= 2 ? NG / 2 : 1;  // groups of half a row's channels
-  uint32_t k[W], v[W];
-  u32x4v vs[GH], vm[GH];
-  uint32_t ks, km;
-
-  __device__ __forceinline__ void load(const char* base, int half, int lane) {
-    typedef uint32_t words __attribute__((ext_vector_type(W)));
-    const words a = *reinterpret_cast<const words*>(base + (half * 64 + lane) * (4 * W));
-    const words b = *reinterpret_cast<const words*>(
-        base + 16 * D + (D == 128 ? (half * 64 + lane) * 16 : lane * 16 + 8 * half));
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      k[i] = a[i];
-      v[i] = b[i];
-    }
-    const char* par = base + 32 * D;
-#pragma unroll
-    for (int i = 0; i < GH; ++i) {
-      const int q = (NG >= 2 ? half * GH : 0) + i;
-      const char* at = par + 128 * (NG + q) + 16 * (lane >> 4);
-      vs[i] = *reinterpret_cast<const u32x4v*>(at);
-      vm[i] = *reinterpret_cast<const u32x4v*>(at + 64);
-    }
-    const int id = half * 64 + lane;  // token id % 32, group id / 32
-    if (id < 32 * NG) {
-      const uint16_t* at =
-          reinterpret_cast<const uint16_t*>(par + 128 * (id / 32)) + kv4_token_slot(id % 32);
-      ks = at[0];
-      km = at[32];
-    }
-  }
-};
-
 // Grid without chunks: 8 x tiles x (units / 8); with: one workgroup per chunk.
-template <int D, int NG, bool BF, bool TREE>
+template <int D, int NG, bool BF>
 __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
   constexpr int J = D / 16, JG = J / NG, CT = D / 32;
   __shared__ Stage<D, NG> lds[2];
@@ -97,82 +55,30 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
   const int c = lane & 31, h = lane >> 5;
   const int ratio = p.q_heads / p.heads;
   Kv4Place w;
-  if (!(p.slots ? kv4_place_chunk<PTC, TREE, false>(p, blockIdx.x, w) : kv4_place_whole(p, w)))
-    return;
+  if (!(p.slots ? kv4_place_chunk<PTC, false>(p, blockIdx.x, w) : kv4_place_whole(p, w))) return;
   const int size = (w.span + w.chunks - 1) / w.chunks;
-  const Kv4Range rg = kv4_range<PTC, TREE>(p, w.s, w.tile, ratio, w.chunk * size,
-                                           w.chunk == w.chunks - 1 ? -1 : (w.chunk + 1) * size);
+  const Kv4Range rg = kv4_range<PTC, false>(p, w.s, w.tile, ratio, w.chunk * size,
+                                     w.chunk == w.chunks - 1 ? -1 : (w.chunk + 1) * size);
   if (rg.i0 >= w.s.n) return;
   const int col = w.tile * PTC + 32 * wave + c, ci = col / ratio;
   const bool live = ci < w.s.n;
   const int qh = w.head * ratio + col % ratio;
   const int row = w.s.first + (live ? ci : 0);
   // tokens seen: column [first, last], any column [lo, hi) (of the wave: [wlo, whi)), every
-  // column of the wave [all_lo, all_hi) (TREE: of those before the tree)
+  // column of the wave [all_lo, all_hi)
   const int last = live ? rg.from + ci : -1;
-  const int first = TREE ? kv4_tree_first(p, w.s, row) : p.window > 0 ? last - p.window + 1 : 0;
+  const int first = p.window > 0 ? last - p.window + 1 : 0;
   const int w0 = (w.tile * PTC + 32 * wave) / ratio;
   const int wl = (w.tile * PTC + 32 * wave + 31) / ratio;
   const int w1 = wl < w.s.n - 1 ? wl : w.s.n - 1;
-  const int whi = w0 < w.s.n ? (TREE ? rg.hi : rg.from + w1 + 1) : 0;
-  const int wlo = TREE ? rg.lo : p.window > 0 ? rg.from + w0 - p.window + 1 : 0;
-  const int all_hi = wl < w.s.n ? (TREE ? rg.from : rg.from + w0 + 1) : 0;
-  const int all_lo = p.window > 0 ? rg.from + (TREE ? w.s.n - 1 : w1) - p.window + 1 : 0;
-
-  // TREE: from here on up to the tree every column of the tile sees a token
-  const int tile_lo = TREE && p.window > 0 ? rg.from + w.s.n - p.window : 0;
+  const int whi = w0 < w.s.n ? rg.from + w1 + 1 : 0;
+  const int wlo = p.window > 0 ? rg.from + w0 - p.window + 1 : 0;
+  const int all_hi = wl < w.s.n ? rg.from + w0 + 1 : 0;
+  const int all_lo = p.window > 0 ? rg.from + w1 - p.window + 1 : 0;
 
   half8v qf[J], qm;
   float cf;
-  {
-    float top = 0.f;
-    u32x4v raw[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      raw[j] = *reinterpret_cast<const u32x4v*>(p.q + (size_t)row * p.ldq + (size_t)qh * D +
-                                                16 * j + 8 * h);
-      float f[8];
-      unpack8<BF>(raw[j], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-    }
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const int d = query_exponent(top);
-    const float up = __builtin_ldexpf(1.f, d);
-    float qsum[NG];
-#pragma unroll
-    for (int q = 0; q < NG; ++q) qsum[q] = 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float f[8], x[8];
-      unpack8<BF>(raw[j], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = f[e] * up;
-        qsum[j / JG] += x[e];
-        if (e & 2) x[e] *= 0.0625f;
-      }
-      qf[j] = __builtin_bit_cast(half8v, pack8<false>(x));
-    }
-    // (sum q) / 2^8 of a group as three fp16 numbers: groups 0, 1 at channels 0..5 of the
-    // operand, groups 2, 3 at 8..13
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-#pragma unroll
-    for (int q = 0; q < NG; ++q) {
-      float y = (qsum[q] + __shfl_xor(qsum[q], 32)) * 0x1p-8f;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float z = lo16<false>(to16<false>(y));
-        y -= z;
-        if (h == q / 2) x[3 * (q & 1) + k] = z;
-      }
-    }
-    qm = __builtin_bit_cast(half8v, pack8<false>(x));
-    // above 0, which would make NaN of a masked logit; what is less leaves nothing of the others
-    cf = fmaxf(__builtin_ldexpf(p.scale * 1.4426950408889634f, 8 - d), 0x1p-126f);
-  }
+  wide_queries<D, NG, BF>(p, row, qh, h, qf, qm, cf);
 
   f32x16 o[CT];
 #pragma unroll
@@ -206,18 +112,11 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
     const int t0 = blk * 32, g = lane >> 4, r = lane & 15;
     if (!valid(blk, pg)) return;  // nobody looks at it
     // what no column sees may be anything: its s and m become 0
-    if (TREE ? t0 < tile_lo || t0 + 32 > rg.from : t0 < rg.lo || t0 + 32 > rg.hi) {
-      uint32_t any = 0;
-      if constexpr (TREE) {
-        for (int i = rg.i0 + lane; i <= rg.i1; i += 64)
-          any |= kv4_tree_sees(p, w.s, w.s.first + i, kv4_tree_first(p, w.s, w.s.first + i), t0);
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) any |= (uint32_t)__shfl_xor((int)any, off);
-      }
+    if (t0 < rg.lo || t0 + 32 > rg.hi) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int t = kv4_slot_token(g, e);
-        if (TREE ? (any >> t & 1u) == 0 : t0 + t < rg.lo || t0 + t >= rg.hi) {
+        const int pos = t0 + kv4_slot_token(g, e);
+        if (pos < rg.lo || pos >= rg.hi) {
           const uint32_t keep = e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
           for (int i = 0; i < Piece<D, NG>::GH; ++i) {
@@ -282,12 +181,10 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
       for (int t = 0; t < CT; ++t) vf[s][t] = __builtin_bit_cast(half8v, st.v[i_blk][s][t][lane]);
     __builtin_amdgcn_sched_barrier(0);
     if (t0 < all_lo || t0 + 32 > all_hi) {
-      uint32_t sees = 0;
-      if constexpr (TREE) sees = live ? kv4_tree_sees(p, w.s, row, first, t0) : 0u;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int t = 4 * h + 8 * (i >> 2) + (i & 3);
-        if (TREE ? (sees >> t & 1u) == 0 : t0 + t < first || t0 + t > last) x[i] = -INFINITY;
+        const int pos = t0 + 4 * h + 8 * (i >> 2) + (i & 3);
+        if (pos < first || pos > last) x[i] = -INFINITY;
       }
     }
     float top = x[0];
@@ -419,13 +316,13 @@ __global__ __launch_bounds__(256, 2) void kv4_prefill_kernel(Kv4AttendArgs p) {
 
 // Joins a tile's chunks, in their order.  Grid: (tiles, D / 8): a workgroup has 8 channels of
 // the tile's 128 columns, a thread 4 of one.
-template <int D, bool BF, bool TREE>
+template <int D, bool BF>
 __global__ __launch_bounds__(256) void kv4_prefill_join_kernel(Kv4AttendArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 31, h = lane >> 5, t = blockIdx.y >> 2, k = blockIdx.y & 3;
   const int ratio = p.q_heads / p.heads;
   Kv4Place w;
-  if (!kv4_place_chunk<PTC, TREE, true>(p, blockIdx.x, w) || w.chunks == 1) return;
+  if (!kv4_place_chunk<PTC, true>(p, blockIdx.x, w) || w.chunks == 1) return;
   const int col = w.tile * PTC + 32 * wave + c, ci = col / ratio;
   if (ci >= w.s.n) return;
   const int qh = w.head * ratio + col % ratio, row = w.s.first + ci;
@@ -452,17 +349,12 @@ __global__ __launch_bounds__(256) void kv4_prefill_join_kernel(Kv4AttendArgs p) 
 }
 
 typedef void (*PrefillFn)(Kv4AttendArgs);
-template <bool BF, bool TREE>
+template <bool BF>
 PrefillFn prefill_kernel(int D, int groups) {
   if (D == 128)
-    return groups == 1 ? kv4_prefill_kernel<128, 1, BF, TREE>
-                       : groups == 2 ? kv4_prefill_kernel<128, 2, BF, TREE>
-                                     : kv4_prefill_kernel<128, 4, BF, TREE>;
-  return groups == 1 ? kv4_prefill_kernel<64, 1, BF, TREE> : kv4_prefill_kernel<64, 2, BF, TREE>;
-}
-template <bool BF, bool TREE>
-PrefillFn join_kernel(int D) {
-  return D == 128 ? kv4_prefill_join_kernel<128, BF, TREE> : kv4_prefill_join_kernel<64, BF, TREE>;
+    return groups == 1 ? kv4_prefill_kernel<128, 1, BF>
+                       : groups == 2 ? kv4_prefill_kernel<128, 2, BF> : kv4_prefill_kernel<128, 4, BF>;
+  return groups == 1 ? kv4_prefill_kernel<64, 1, BF> : kv4_prefill_kernel<64, 2, BF>;
 }
 
 }  // namespace
@@ -470,16 +362,12 @@ PrefillFn join_kernel(int D) {
 hipError_t launch_kv4_prefill(const Kv4AttendArgs& a, int D, int groups, bool bf, hipStream_t st) {
   const long long units = ((long long)a.heads * a.batch + 7) / 8 * 8;
   const unsigned grid = a.slots ? a.slots : (unsigned)(units * a.col_tiles);
-  const bool tree = a.mask != nullptr;
-  const PrefillFn fn = bf ? (tree ? prefill_kernel<true, true>(D, groups)
-                                  : prefill_kernel<true, false>(D, groups))
-                          : (tree ? prefill_kernel<false, true>(D, groups)
-                                  : prefill_kernel<false, false>(D, groups));
-  hipLaunchKernelGGL(fn, kv4_grid(grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(bf ? prefill_kernel<true>(D, groups) : prefill_kernel<false>(D, groups),
+                     kv4_grid(grid), dim3(256), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.slots == 0) return e;
-  const PrefillFn join = bf ? (tree ? join_kernel<true, true>(D) : join_kernel<true, false>(D))
-                            : (tree ? join_kernel<false, true>(D) : join_kernel<false, false>(D));
+  auto join = D == 128 ? (bf ? kv4_prefill_join_kernel<128, true> : kv4_prefill_join_kernel<128, false>)
+                       : (bf ? kv4_prefill_join_kernel<64, true> : kv4_prefill_join_kernel<64, false>);
   hipLaunchKernelGGL(join, dim3(a.tiles, D / 8), dim3(256), 0, st, a);
   return hipGetLastError();
 }
