@@ -1003,7 +1003,7 @@ int kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
   int* cnt;
   float* part;
   if ((rc = get_workspace(dev, st, plan.counters, plan.floats, &cnt, &part, KV4_STRIPES,
-                          kv4_attend_most_floats(plan.cols, head))))
+                          kv4_attend_most_floats(tree ? 128 : plan.cols, head))))
     return rc;
   Kv4AttendArgs a{};
   a.q = q;

@@ -132,7 +132,7 @@ __device__ __forceinline__ uint32_t wave_sums(uint32_t x) {
 // workgroup has two.
 template <int TC, bool TREE>
 struct Kv4Stripes {
-  static constexpr int kLead = TC == 128 ? 4 : 16;
+  static constexpr int kLead = TC >= 128 ? 4 : 16;
   uint32_t total, stripe;
   int lead;
 

@@ -563,6 +563,23 @@ AttendFn attend_kernel(int cols, bool bf, int D, int groups) {
   return bf ? attend_kernel<16, true, TREE>(D, groups) : attend_kernel<16, false, TREE>(D, groups);
 }
 
+// Tiles of 128 columns for a tree's, or of 16?  A block takes a workgroup 0.42 us in a tile of 16
+// and 2 us in one of 128; a tile costs 10 and 4 blocks more, and tiles of 128 another 19 us to hand
+// over and join (38, since the lengths are half of what they may be).  16 against 128, 64 query
+// heads on 8, us: 128 columns, contexts to 8 x 8192 / 1 x 32768 / 32 x 2048 / 64 x 300 tokens
+// 64 / 60 / 74 / 59 against 59 / 81 / 59 / 34; 96 columns, 8 x 8192 / 32 x 2048: 41 / 55 against
+// 50 / 52; 104 columns, 2 x 131072: 289 against 237; 64 columns, 8 x 8192 / 4 x 131072: 40 / 246
+// against 52 / 287.
+bool wide_tree(int batch, long long columns, int max_new, int max_len, int heads, int window) {
+  double span = (max_len + 31.0) / 32;
+  const double near = ((double)window + max_new) / 32 + 2;
+  if (window > 0 && span > near) span = near;
+  const double units = (double)batch * heads;
+  const double narrow = 0.42 * units * (double)((columns + 15) / 16) * (span + 10);
+  const double wide = 2.0 * units * (double)((columns + 127) / 128) * (span + 4) + 38.0 * KV4_STRIPES;
+  return wide < narrow;
+}
+
 }  // namespace
 
 size_t kv4_attend_most_floats(int cols, int D) {
@@ -576,6 +593,7 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
   const int ratio = q_heads / heads;
   const long long columns = (long long)max_new * ratio;
   p.cols = columns <= 8 ? 8 : columns <= kPrefillColumns ? 16 : 128;
+  if (tree && columns > 8) p.cols = wide_tree(batch, columns, max_new, max_len, heads, window) ? 128 : 16;
   p.col_tiles = (int)((columns + p.cols - 1) / p.cols);
   // tiles there can be: each sequence rounds up, and rows are not shared
   long long tiles = ((long long)tokens * ratio + p.cols - 1) / p.cols + batch;
