@@ -267,3 +267,31 @@ def test_compact_in_a_graph(lib):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(pool.dev, want) and out.tolist() == [34, 14]
+
+
+# ---- past 4 GiB -------------------------------------------------------------------------------------
+def test_layers_past_4_gib(lib):
+    """Two layers 5 GiB apart, pages in the last of each layer's bytes: the same tokens move, the same page is
+    copied as in a small pool."""
+    heads, D, G, page = 8, 128, 64, 256
+    size = lib.w4a16_kv4_page_bytes(heads, D, G, page)
+    pages = (5 << 30) // size
+    stride = pages * size
+    big = torch.zeros(2 * stride, dtype=torch.uint8, device="cuda").view(2, pages, size)
+    ids = [pages - 1, pages - 3, 5]
+    small = Pool(2, 3, heads, D, G, page, 1, gap=0)
+    big[:, ids] = small.dev.view(2, 3, size)
+    spread, path, count = [(40, 270)], [[0, 9, 11, 39]], [4]  # the tree begins in one page and ends in another
+    check_compact(lib, small, spread, [[0, 1, -1]], path, count)
+    out = i32([0])
+    lib.w4a16_kv4_compact(big, i32(path), i32(count), i32([0, 40]), i32([270]), i32([[ids[0], ids[1], -1]]), out, 1, 40, 40, 4, 2, stride, heads, D, G,
+                          page, pages, 3)
+    assert out.item() == 234 and torch.equal(big[:, ids], small.dev.view(2, 3, size))
+    # page `pages - 2` is the only free one
+    pinned = torch.ones(pages, dtype=torch.uint8, device="cuda")
+    pinned[pages - 2] = 0
+    table, held, missing = torch.zeros(1, 2, dtype=torch.int32, device="cuda"), i32([0]), i32([7])
+    lib.w4a16_kv4_fork(big, i32([[ids[0], ids[1]]]), i32([300]), i32([0]), None, None, pinned, table, held, missing, 1, 1, 2, stride, heads, D, G, page, pages, 2)
+    assert table.tolist() == [[ids[0], pages - 2]] and missing.item() == 0
+    blocks = big.view(2, pages, heads, page // 32, -1)
+    assert torch.equal(blocks[:, pages - 2, :, :2], blocks[:, ids[1], :, :2]) and (blocks[:, pages - 2, :, 2:] == 0).all()

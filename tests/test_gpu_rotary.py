@@ -166,3 +166,15 @@ def test_side_stream_and_graph(lib):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(now, out))
+
+
+def test_rows_past_4_gib(lib):
+    c = Case(24, 2, 1, 64, 64, 1, F16, seed=9)
+    ld = (1 << 27) + 8  # 24 rows of 256 MiB
+    far = torch.empty(23 * ld + 128, dtype=F16, device="cuda").as_strided((24, 128), (ld, 1))
+    far.copy_(c.parts(c.x)[0])
+    k = c.parts(c.x)[1].contiguous().cuda()
+    args = c.pos.cuda(), None, c.freq.cuda()
+    lib.w4a16_rotary(far, k, *args, far, k, 24, 2, 1, 64, 64, 1, 27, ld, 64, ld, 64)
+    _, qo, ko = c.run(lib)
+    assert torch.equal(far, qo[:, :128]) and torch.equal(k, ko[:, :64])

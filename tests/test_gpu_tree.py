@@ -350,3 +350,21 @@ def test_callers_workspace(lib):
             assert e.value.code == -6
         finally:
             lib.w4a16_set_workspace(None, 0, side)
+
+
+@pytest.mark.parametrize("ratio,most", [(2, None), (16, 60000)])
+def test_pages_past_4_gib(lib, ratio, most):
+    """The same pages at the end of a cache of 5 GiB give the same bits."""
+    s = Trees([(40, 200), (30, 90)], 8, ratio, 128, 64, 64, F16, seed=14)
+    s.masks()
+    out, lse = s.run(lib, most)
+    size = s.raw.shape[1]
+    pages = (5 << 30) // size
+    big = torch.zeros(pages, size, dtype=torch.uint8, device="cuda")
+    big[pages - s.pages:] = s.dev[3]
+    table = torch.where(s.dev[2] >= 0, s.dev[2] + (pages - s.pages), -1).to(torch.int32)
+    w = 8 * ratio * 128
+    o, l = torch.zeros_like(out), torch.zeros_like(lse)
+    lib.w4a16_kv4_tree_attention(s.q.cuda(), s.dev[0], s.dev[1], table, big, s.dev[4], None, o, l, 2, s.tokens, s.max_new, most or s.max_len, s.words,
+                                 w + 8, w + 16, 8 * ratio, 8, 128, 64, 64, pages, s.width, 0, 128 ** -0.5)
+    assert torch.equal(o[:, :w], out[:, :w]) and torch.equal(l, lse)

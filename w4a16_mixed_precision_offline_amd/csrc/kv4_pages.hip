@@ -310,93 +310,93 @@ __global__ __launch_bounds__(256) void kv4_compact_kernel(Kv4CompactArgs p, int 
     go = go && src_page >= 0 && dst_page >= 0;
     const uint32_t goes = (uint32_t)__ballot(go) & 0xFFu;
     if (goes == 0) continue;
-    const int src_off = (src >> 5) % page_blocks, dst_off = (dst >> 5) % page_blocks;
+    // bytes from a head's first page to the blocks, the same for every unit
+    auto block_at = [&](int page, int pos) {
+      return (size_t)(page < 0 ? 0 : page) * p.heads * head_bytes +
+             (size_t)((pos >> 5) % page_blocks) * kv4_block_bytes(D, NG);
+    };
+    const size_t src_at = block_at(src_page, src), dst_at = block_at(dst_page, dst);
+    auto of_lane = [](size_t x, int l) {
+      return (size_t)(uint32_t)__builtin_amdgcn_readlane((int)x, l) |
+             (size_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), l) << 32;
+    };
+    auto of_each = [](size_t x, int l) {
+      return (size_t)(uint32_t)__shfl((int)x, l) | (size_t)(uint32_t)__shfl((int)(x >> 32), l) << 32;
+    };
+    // K: lane 4 i + g < 32 has run g of node i; parameters: lanes 8 i .. 8 i + 7 have node i's
+    typedef uint32_t run __attribute__((ext_vector_type(W)));
+    const int ki = (lane >> 2) & 7, pi = lane >> 3;
+    const bool kgo = lane < 32 && (goes >> ki & 1u) != 0, pgo = (goes >> pi & 1u) != 0;
+    auto k_place = [&](int pos) {
+      return (size_t)(((pos >> 4 & 1) * 64 + 16 * (lane & 3) + (pos & 15)) * W * 4);
+    };
+    constexpr int NP = 4 * NG;  // K's and V's s and m of each group
+    auto p_place = [&](int pos) {
+      return (size_t)(32 * D + 2 * ((lane & 7) * 32 + kv4_token_slot(pos & 31)));
+    };
+    const size_t k_src = of_each(src_at, ki) + k_place(__shfl(src, ki));
+    const size_t k_dst = of_each(dst_at, ki) + k_place(__shfl(dst, ki));
+    const size_t p_src = of_each(src_at, pi) + p_place(__shfl(src, pi));
+    const size_t p_dst = of_each(dst_at, pi) + p_place(__shfl(dst, pi));
+    // V: channels 64 h + lane; the words of a block of lane group tg
+    const int v_lane = 16 * D + ((lane & 15) * 4 + (lane >> 4)) * 4;
+    const int d0 = from + j0, skew = d0 & 3;
+    // the places of nodes j0 .. j0 + 7 that lie in group y of four, which share a word
+    auto group_of = [&](int y) { return goes & (uint32_t)((0xFULL << (4 * y)) >> skew); };
     for (int unit = wave; unit < p.layers * p.heads; unit += waves) {
       char* base = p.cache + (size_t)(unit / p.heads) * p.stride +
                    (size_t)(unit % p.heads) * head_bytes;
-      auto block = [&](int page, int off, int l) {
-        return base + (size_t)__builtin_amdgcn_readlane(page, l) * p.heads * head_bytes +
-               (size_t)__builtin_amdgcn_readlane(off, l) * kv4_block_bytes(D, NG);
-      };
-      // K: lane 4 i + g has run g of token i; parameters: lane 8 i + .. has some of token i
-      typedef uint32_t run __attribute__((ext_vector_type(W)));
-      auto at_lane = [&](int x, int l) { return __shfl(x, l); };
-      const int ki = (lane >> 2) & 7, kg = lane & 3;
-      const bool kgo = lane < 32 && (goes >> ki & 1u) != 0;
-      const int ksp = at_lane(src_page, ki), kso = at_lane(src_off, ki), kst = at_lane(src, ki) & 31;
-      const int kdp = at_lane(dst_page, ki), kdo = at_lane(dst_off, ki), kdt = at_lane(dst, ki) & 31;
-      auto k_run = [&](int page, int off, int t) {
-        return reinterpret_cast<run*>(base + (size_t)page * p.heads * head_bytes +
-                                      (size_t)off * kv4_block_bytes(D, NG) +
-                                      (((t >> 4) * 64 + 16 * kg + (t & 15)) * W) * 4);
-      };
       run kw;
-      if (kgo) kw = *k_run(ksp, kso, kst);
-      const int pi = lane >> 3;
-      const bool pgo = (goes >> pi & 1u) != 0;
-      const int psp = at_lane(src_page, pi), pso = at_lane(src_off, pi), pst = at_lane(src, pi) & 31;
-      const int pdp = at_lane(dst_page, pi), pdo = at_lane(dst_off, pi), pdt = at_lane(dst, pi) & 31;
-      constexpr int NP = 4 * NG;  // K's and V's s and m of each group
+      if (kgo) kw = *reinterpret_cast<const run*>(base + k_src);
       uint16_t par[(NP + 7) / 8];
-      auto params = [&](int page, int off, int t, int i) {
-        return reinterpret_cast<uint16_t*>(base + (size_t)page * p.heads * head_bytes +
-                                           (size_t)off * kv4_block_bytes(D, NG) + 32 * D) +
-               i * 32 + kv4_token_slot(t);
-      };
 #pragma unroll
       for (int i = 0; i < (NP + 7) / 8; ++i)
-        if (pgo && 8 * i + (lane & 7) < NP) par[i] = *params(psp, pso, pst, 8 * i + (lane & 7));
-      // V: word of channel c = 64 h + lane and lane group tg of a block
-      auto v_word = [&](char* blk, int h, int tg) {
-        return reinterpret_cast<uint32_t*>(blk + 16 * D) +
-               (h * 64 + 16 * tg + (lane & 15)) * 4 + (lane >> 4);
-      };
+        if (pgo && 8 * i + (lane & 7) < NP)
+          par[i] = *reinterpret_cast<const uint16_t*>(base + p_src + 512 * i);
       uint32_t code[D / 64][8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (goes >> i & 1u) {
-          const int t = __builtin_amdgcn_readlane(src, i) & 31;
+          const int tg = (__builtin_amdgcn_readlane(src, i) >> 2) & 3;
+          const char* at = base + of_lane(src_at, i) + 256 * tg;
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            code[h][i] = *v_word(block(src_page, src_off, i), h, (t >> 2) & 3);
+            code[h][i] = *reinterpret_cast<const uint32_t*>(at + v_lane + 1024 * h);
         }
-      // the words of the places: those of nodes j0 .. j0 + 7 that go into group y of four places
-      const int d0 = from + j0, skew = d0 & 3;
-      uint32_t word[D / 64][3];
-      uint32_t* at[3][D / 64];
+      uint32_t word[3][D / 64];
 #pragma unroll
-      for (int y = 0; y < 3; ++y) {
-        const uint32_t in = goes & (uint32_t)((0xFULL << (4 * y)) >> skew);
-        if (in == 0) continue;
-        const int i = __builtin_ctz(in);
-        char* blk = block(dst_page, dst_off, i);
+      for (int y = 0; y < 3; ++y)
+        if (const uint32_t in = group_of(y)) {
+          const int i = __builtin_ctz(in);
+          const char* at = base + of_lane(dst_at, i) + 256 * (((d0 + i) >> 2) & 3);
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          at[y][h] = v_word(blk, h, ((d0 + i) >> 2) & 3);
-          word[h][y] = *at[y][h];
+          for (int h = 0; h < D / 64; ++h)
+            word[y][h] = *reinterpret_cast<const uint32_t*>(at + v_lane + 1024 * h);
         }
-      }
-      if (kgo) *k_run(kdp, kdo, kdt) = kw;
+      if (kgo) *reinterpret_cast<run*>(base + k_dst) = kw;
 #pragma unroll
       for (int i = 0; i < (NP + 7) / 8; ++i)
-        if (pgo && 8 * i + (lane & 7) < NP) *params(pdp, pdo, pdt, 8 * i + (lane & 7)) = par[i];
+        if (pgo && 8 * i + (lane & 7) < NP)
+          *reinterpret_cast<uint16_t*>(base + p_dst + 512 * i) = par[i];
 #pragma unroll
-      for (int y = 0; y < 3; ++y) {
-        const uint32_t in = goes & (uint32_t)((0xFULL << (4 * y)) >> skew);
-        if (in == 0) continue;
+      for (int y = 0; y < 3; ++y)
+        if (const uint32_t in = group_of(y)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if ((in >> i & 1u) == 0) continue;
-          const int ts = __builtin_amdgcn_readlane(src, i), td = d0 + i;
-          const int ss = 4 * nib_pos(((ts >> 4) & 1) * 4 + (ts & 3));
-          const int sd = 4 * nib_pos(((td >> 4) & 1) * 4 + (td & 3));
+          for (int i = 0; i < 8; ++i) {
+            if ((in >> i & 1u) == 0) continue;
+            const int ts = __builtin_amdgcn_readlane(src, i), td = d0 + i;
+            const int ss = 4 * nib_pos(((ts >> 4) & 1) * 4 + (ts & 3));
+            const int sd = 4 * nib_pos(((td >> 4) & 1) * 4 + (td & 3));
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              word[y][h] = (word[y][h] & ~(15u << sd)) | ((code[h][i] >> ss & 15u) << sd);
+          }
+          const int i = __builtin_ctz(in);
+          char* at = base + of_lane(dst_at, i) + 256 * (((d0 + i) >> 2) & 3);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            word[h][y] = (word[h][y] & ~(15u << sd)) | ((code[h][i] >> ss & 15u) << sd);
+            *reinterpret_cast<uint32_t*>(at + v_lane + 1024 * h) = word[y][h];
         }
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) *at[y][h] = word[h][y];
-      }
     }
   }
 }
@@ -430,10 +430,11 @@ hipError_t launch_kv4_fork(const Kv4ForkArgs& a, int D, int groups, hipStream_t 
 }
 
 hipError_t launch_kv4_compact(const Kv4CompactArgs& a, int D, int groups, hipStream_t st) {
-  // units of a wave: as many as leave 8192 waves, 4 at most
+  // Units of a wave: two where that leaves 8192 waves.  1 / 2 / 4 / 8 / 16 units a wave: 40 / 38 / 40 /
+  // 49 / 70 us for 48 sequences, 64 layers of 8 heads.
   const int units = a.layers * a.heads;
   long long each = (long long)units * a.batch / 8192;
-  each = each < 1 ? 1 : each > 4 ? 4 : each;
+  each = each < 1 ? 1 : each > 2 ? 2 : each;
   const int groups4 = (int)((units + 4 * each - 1) / (4 * each));
   auto fn = D == 128 ? (groups == 1   ? kv4_compact_kernel<128, 1>
                         : groups == 2 ? kv4_compact_kernel<128, 2>

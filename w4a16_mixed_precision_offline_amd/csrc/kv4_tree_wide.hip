@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
     if (blk < b1) {
       int pg = look_up(blk + mine), next = look_up(blk + WS + mine);
       fetch(blk + mine, pg);
-      if (again) __syncthreads();  // the last tile's stages are no longer read
+      __syncthreads();  // m is cleared, or the last tile's stages are no longer read
       for (int buf = 0;; buf ^= 1) {
         unpack(lds[buf], blk + mine, pg);
         __syncthreads();
