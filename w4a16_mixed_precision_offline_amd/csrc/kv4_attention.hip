@@ -631,6 +631,7 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     if (!wide && (batch > 1024 || stripes <= tiles)) return p;
     if (stripes > KV4_STRIPES) stripes = KV4_STRIPES;
     p.target = (int)stripes;
+    p.tiles = tiles < (1 << 24) ? (int)tiles : 1 << 24;
     p.slots = 2 * (int)stripes;
     if (!wide) p.counters = (size_t)stripes;
     else if (stripes == 1) p.slots = 0;  // nothing to join

@@ -322,58 +322,59 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
 }
 
 // Joins the parts of the tile that starts in a stripe and goes on past it, if there is one.
-// Grid: (stripes, D / 32): a workgroup has 32 channels of the tile's 128 columns, a thread 16 of
-// one (8 channels a workgroup, four times as many of them: 23 us instead of
-// 14 on 16 trees of up to 64 nodes).
-template <int D, bool BF>
+// Grid: (D / (8 KN), stripes): a workgroup has 8 KN channels of the tile's 128 columns, a thread
+// 4 KN of one.  The channels go first, since workgroups go round robin to the 8 XCDs: tiles of
+// even lengths start in stripes that one XCD would have all of.
+template <int D, bool BF, int KN>
 __global__ __launch_bounds__(256) void kv4_tree_join_kernel(Kv4AttendArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = lane & 31, h = lane >> 5, t = blockIdx.y;
+  const int c = lane & 31, h = lane >> 5, t = blockIdx.x * KN / 4, k0 = blockIdx.x * KN % 4;
+  const uint32_t first = blockIdx.y;
   const int ratio = p.q_heads / p.heads;
   Kv4Stripes<PTC, true> stripes;
   typename Kv4Stripes<PTC, true>::Lane lanes = stripes.init(p, ratio);
-  const uint32_t end = (blockIdx.x + 1) * stripes.stripe;
+  const uint32_t end = (first + 1) * stripes.stripe;
   if (end >= stripes.total) return;
   Kv4Seq seq;
   int b, head, tile, span;
   uint32_t u0;
   stripes.find(p, end - 1, ratio, lanes, seq, b, head, tile, span, u0);
   u0 += stripes.lead;
-  if (u0 / stripes.stripe != blockIdx.x || u0 + span <= end) return;
+  if (u0 / stripes.stripe != first || u0 + span <= end) return;
   const uint32_t last = (u0 + span - 1) / stripes.stripe;
   const int col = tile * PTC + 32 * wave + c, ci = col / ratio;
   if (ci >= seq.n) return;
   const int qh = head * ratio + col % ratio, row = seq.first + ci;
   float m = kKv4None, l = 0.f;
-  f32x4 o[4];
+  f32x4 o[KN];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) o[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (uint32_t i = blockIdx.x; i <= last; ++i) {
-    const size_t slot = 2 * (size_t)i + (i == blockIdx.x);
+  for (int k = 0; k < KN; ++k) o[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16 / KN
+  for (uint32_t i = first; i <= last; ++i) {
+    const size_t slot = 2 * (size_t)i + (i == first);
     const float* ml = p.part_ml + (slot * PTC + 32 * wave + c) * 2;
     const f32x4* at = reinterpret_cast<const f32x4*>(p.part_o + slot * PTC * D) +
-                      (wave * (D / 32) + t) * 4 * 64 + lane;
-    f32x4 v[4];
+                      ((wave * (D / 32) + t) * 4 + k0) * 64 + lane;
+    f32x4 v[KN];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = at[64 * k];
+    for (int k = 0; k < KN; ++k) v[k] = at[64 * k];
     const float cm = ml[0], cl = ml[1];
     const float next = fmaxf(m, cm);
     const float a = __builtin_amdgcn_exp2f(m - next), f = __builtin_amdgcn_exp2f(cm - next);
     m = next;
     l = l * a + cl * f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = o[k] * a + v[k] * f;
+    for (int k = 0; k < KN; ++k) o[k] = o[k] * a + v[k] * f;
   }
   const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  uint16_t* dst = p.out + (size_t)row * p.ldo + (size_t)qh * D + 32 * t + 4 * h;
+  uint16_t* dst = p.out + (size_t)row * p.ldo + (size_t)qh * D + 32 * t + 8 * k0 + 4 * h;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < KN; ++k) {
     o[k] *= inv;
     *reinterpret_cast<u32x2v*>(dst + 8 * k) =
         u32x2v{pack16<BF>(o[k][0], o[k][1]), pack16<BF>(o[k][2], o[k][3])};
   }
-  if (blockIdx.y == 0 && h == 0 && p.lse != nullptr)
+  if (blockIdx.x == 0 && h == 0 && p.lse != nullptr)
     p.lse[(size_t)row * p.q_heads + qh] = (m + log2f(l) - kKv4Lift) * 0.6931471805599453f;
 }
 
@@ -386,9 +387,10 @@ TreeFn tree_kernel(int D, int groups) {
                          : kv4_tree_wide_kernel<128, 4, BF>;
   return groups == 1 ? kv4_tree_wide_kernel<64, 1, BF> : kv4_tree_wide_kernel<64, 2, BF>;
 }
-template <bool BF>
-TreeFn join_kernel(int D) {
-  return D == 128 ? kv4_tree_join_kernel<128, BF> : kv4_tree_join_kernel<64, BF>;
+template <int KN>
+TreeFn join_kernel(int D, bool bf) {
+  if (D == 128) return bf ? kv4_tree_join_kernel<128, true, KN> : kv4_tree_join_kernel<128, false, KN>;
+  return bf ? kv4_tree_join_kernel<64, true, KN> : kv4_tree_join_kernel<64, false, KN>;
 }
 
 }  // namespace
@@ -399,8 +401,13 @@ hipError_t launch_kv4_tree_wide(const Kv4AttendArgs& a, int D, int groups, bool 
                      dim3(a.target), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.target == 1) return e;
-  hipLaunchKernelGGL(bf ? join_kernel<true>(D) : join_kernel<false>(D), dim3(a.target, D / 32),
-                     dim3(256), 0, st, a);
+  // Many tiles of few parts: 32 channels a workgroup (16 trees of up to 64 nodes: 23 us with 8 to a
+  // workgroup, 15 with 32).  Few tiles of many parts: 8 (two trees of 13 nodes to 131072, 32 parts
+  // a tile: JOINFIG).
+  if (a.target >= 8 * a.tiles)
+    hipLaunchKernelGGL(join_kernel<1>(D, bf), dim3(D / 8, a.target), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(join_kernel<4>(D, bf), dim3(D / 32, a.target), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
