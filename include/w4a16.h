@@ -563,7 +563,7 @@ int w4a16_kv4_fork(void* cache, const int32_t* table, const int32_t* lens, const
  *     0 .. axes - 1, may be NULL with one axis; freq (device, in) fp32 [rot / 2], radians per
  *     position; with -freq the rotation is undone, which is also its gradient.
  *   Angles are formed in 64 bits, so positions may be any int32; the rest is fp32 and each result
- *   is rounded once.  16 <= rot <= head <= 512, rot % 16 == 0, head % 8 == 0, tokens <= 2^25,
+ *   is rounded once.  16 <= rot <= head <= 512, rot % 16 == 0, head % 8 == 0, tokens < 2^24,
  *   (q_heads + kv_heads) * head <= 2^24. */
 #define W4A16_ROTARY_HALVES     0
 #define W4A16_ROTARY_NEIGHBOURS 1

@@ -76,7 +76,7 @@ def test_fork_refusals(code, change):
 @pytest.mark.parametrize("code,change", [
     *[(NULL, {n: None}) for n in ("q", "k", "pos", "freq", "qo", "ko", "axis")], *[(ALIGN, {n: MIS}) for n in ("q", "k", "pos", "axis", "freq")],
     (ALIGN, dict(q=264, qo=264)), (ALIGN, dict(ko=264)),
-    (SHAPE, dict(tokens=0)), (SHAPE, dict(tokens=(1 << 25) + 1, ldpos=1 << 26)), (SHAPE, dict(q_heads=0)), (SHAPE, dict(kv_heads=-1)),
+    (SHAPE, dict(tokens=0)), (SHAPE, dict(tokens=1 << 24, ldpos=1 << 26)), (SHAPE, dict(q_heads=0)), (SHAPE, dict(kv_heads=-1)),
     (SHAPE, dict(head=8, rot=8)), (SHAPE, dict(head=60, rot=48)), (SHAPE, dict(head=520)), (SHAPE, dict(rot=0)), (SHAPE, dict(rot=8)),
     (SHAPE, dict(rot=40)), (SHAPE, dict(rot=80)), (SHAPE, dict(axes=0)), (SHAPE, dict(ldpos=3)), (SHAPE, dict(ldq=248)),
     (SHAPE, dict(ldq=260, ldqo=260)), (SHAPE, dict(ldk=120)), (SHAPE, dict(ldqo=264)), (SHAPE, dict(ldko=136)),

@@ -276,7 +276,8 @@ struct Kv4CompactArgs {
 hipError_t launch_kv4_compact(const Kv4CompactArgs& a, int D, int groups, hipStream_t st);
 
 // rotary.hip; axis may be NULL (one axis), k and ko with kv_heads 0
-constexpr int ROTARY_MAX_HEAD = 512, ROTARY_MAX_TOKENS = 1 << 25;
+// (a launch of 2^32 threads in a dimension wraps: tokens of 256)
+constexpr int ROTARY_MAX_HEAD = 512, ROTARY_MAX_TOKENS = (1 << 24) - 1;
 struct RotaryArgs {
   const uint16_t *q, *k;
   const int *pos, *axis;

@@ -162,8 +162,8 @@ struct Kv4Stripes {
     x.size = (uint32_t)x.tiles * p.heads * tile_size(x.span);
     x.upto = wave_sums(x.size);
   }
-  // Returns the lanes of the first 64 sequences.
-  __device__ __forceinline__ Lane init(const Kv4AttendArgs& p, int ratio) {
+  // n: how many stripes.  Returns the lanes of the first 64 sequences.
+  __device__ __forceinline__ Lane init(const Kv4AttendArgs& p, int ratio, uint32_t n) {
     lead = 0;
     stripe = p.chunk;
     total = 0;
@@ -172,7 +172,7 @@ struct Kv4Stripes {
       x = fetch(p, b0, ratio);
       total += __builtin_amdgcn_readlane(x.upto, 63);
     }
-    if (total <= stripe * gridDim.x) return x;
+    if (total <= stripe * n) return x;
     lead = kLead;
     total = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 64) {
@@ -180,7 +180,7 @@ struct Kv4Stripes {
       else resize(p, x);
       total += __builtin_amdgcn_readlane(x.upto, 63);
     }
-    stripe = (total + gridDim.x - 1) / gridDim.x;
+    stripe = (total + n - 1) / n;
     return x;
   }
   // The tile at place `at` (< total); u0: where it starts, x: lanes of the first 64 sequences

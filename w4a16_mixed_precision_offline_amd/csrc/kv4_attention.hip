@@ -124,7 +124,7 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
   typename Kv4Stripes<TC, TREE>::Lane lanes;
   uint32_t pos = 0, stop = 1;
   if (p.slots) {
-    lanes = stripes.init(p, ratio);
+    lanes = stripes.init(p, ratio, gridDim.x);
     pos = blockIdx.x * stripes.stripe;
     stop = pos + stripes.stripe < stripes.total ? pos + stripes.stripe : stripes.total;
   }
@@ -563,20 +563,22 @@ AttendFn attend_kernel(int cols, bool bf, int D, int groups) {
   return bf ? attend_kernel<16, true, TREE>(D, groups) : attend_kernel<16, false, TREE>(D, groups);
 }
 
-// Tiles of 128 columns for a tree's, or of 16?  A block takes a workgroup 0.42 us in a tile of 16
-// and 2 us in one of 128; a tile costs 10 and 4 blocks more, and tiles of 128 another 19 us to hand
-// over and join (38, since the lengths are half of what they may be).  16 against 128, 64 query
-// heads on 8, us: 128 columns, contexts to 8 x 8192 / 1 x 32768 / 32 x 2048 / 64 x 300 tokens
-// 64 / 60 / 74 / 59 against 59 / 81 / 59 / 34; 96 columns, 8 x 8192 / 32 x 2048: 41 / 55 against
-// 50 / 52; 104 columns, 2 x 131072: 289 against 237; 64 columns, 8 x 8192 / 4 x 131072: 40 / 246
-// against 52 / 287.
+// Tiles of 128 columns for trees, or of 16?  A block takes a workgroup 0.42 us in a tile of 16 and
+// 2 us in one of 128, a tile costs 10 and 4 blocks more, and tiles of 128 take 11 us more to hand
+// over and join; of several sequences the lengths are taken for half of what they may be.  16
+// against 128, 64 query heads on 8, us: 128 columns, contexts to 8 x 8192 / 1 x 32768 / 32 x 2048 /
+// 64 x 300 / 1 x 1000 tokens 64 / 60 / 74 / 59 / 13 against 56 / 52 / 52 / 33 / 20; 96 columns, 8 x
+// 8192 / 32 x 2048 / 1 x 32768: 41 / 55 / 55 against 47 / 46 / 49; 104 columns, 2 x 131072: 289
+// against 217; 64 columns, 8 x 8192 / 4 x 131072: 40 / 246 against 51 / 295; 512 columns, 1 x 4000:
+// 41 against 35.
 bool wide_tree(int batch, long long columns, int max_new, int max_len, int heads, int window) {
   double span = (max_len + 31.0) / 32;
+  if (batch > 1) span /= 2;
   const double near = ((double)window + max_new) / 32 + 2;
   if (window > 0 && span > near) span = near;
   const double units = (double)batch * heads;
   const double narrow = 0.42 * units * (double)((columns + 15) / 16) * (span + 10);
-  const double wide = 2.0 * units * (double)((columns + 127) / 128) * (span + 4) + 38.0 * KV4_STRIPES;
+  const double wide = 2.0 * units * (double)((columns + 127) / 128) * (span + 4) + 11.0 * KV4_STRIPES;
   return wide < narrow;
 }
 
@@ -625,7 +627,9 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     // on 8 kv heads 9.5 / 10.2 / 11.7 / 11.5, of 4000 13.8 / 11.6 / 11.8 / 14.8, of 16000 25.4 /
     // 25.9 / 16.5 / 16.6; six to 4000 15.9 / 15.2 / 12.5 / 15.3, to 16000 26 each; 24 to 1000
     // 16.1 / 16.1 / 16.0 / 12.5, to 16000 55 each.
-    p.chunk = p.cols == 128 ? 16 : 8;
+    // Tiles of 128 columns (trees), 4 / 8 / 16: 512 columns over 4000 tokens 38 / 35 / 37, 128 over
+    // 4000 21 / 22 / 32, over 32768 52 / 52 / 51.
+    p.chunk = 8;
     long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
     const bool wide = p.cols == 128;  // trees only: always stripes
     if (!wide && (batch > 1024 || stripes <= tiles)) return p;

@@ -8,6 +8,20 @@
 //
 // What each of a block's tokens is to each column is worked out once, by the waves that unpack the
 // block: 32 bits a column in LDS, where the block reaches into the tree or out of the window.
+//
+// Bound: matrix and vector instructions, of which the card overlaps two fifths at best (a probe
+// of alternating phases, two waves to a SIMD: 644 ns where 432 and 360 are the parts).  Tiles
+// all full and of equal length (16 sequences of 64 nodes and 8192 tokens, 64 query heads on 8 of
+// 128 channels, groups of 64): 275 GFLOP in 500 us, 0.55 PFLOP/s (bf16 rows 403 us; groups of 128
+// 477 us; a large fp16 product runs at 1.16).  Parts of it left out: the second part of p 100 us,
+// LDS reads 93, unpacking and its loads 85, exponentials and sums 38; one workgroup to a compute
+// unit instead of two 707.  32 to 64 nodes and up to 8192 tokens: 100 GFLOP in 216 us, of which 5
+// join the parts; two trees of 13 nodes, contexts of 131072 and less, groups of 32: 157 us.
+// Registers: 234 with groups of 64 (places in LDS and in the pages are worked out again for each
+// stage: kept, they made 256 and spills).  2 are spilled with groups of 32.
+// Measured, not kept: 8 waves of 32 columns over one stage (478 us where 513, but half-empty tiles
+// of 256: 272 us where 250); K's operands read ahead of the block before, or of the unpacking, and
+// no barriers for the scheduler (no difference within 3%).
 #include "kv4_wide.h"
 
 namespace w4a16 {
@@ -52,7 +66,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
     lds[i / (WS * 64)].m[i / 64 % WS][i % 64] = u32x4v{0u, 0u, 0u, 0u};
 
   Kv4Stripes<PTC, true> stripes;
-  typename Kv4Stripes<PTC, true>::Lane lanes = stripes.init(p, ratio);
+  typename Kv4Stripes<PTC, true>::Lane lanes = stripes.init(p, ratio, gridDim.x);
   uint32_t place = blockIdx.x * stripes.stripe;
   const uint32_t stop =
       place + stripes.stripe < stripes.total ? place + stripes.stripe : stripes.total;
@@ -332,7 +346,7 @@ __global__ __launch_bounds__(256) void kv4_tree_join_kernel(Kv4AttendArgs p) {
   const uint32_t first = blockIdx.y;
   const int ratio = p.q_heads / p.heads;
   Kv4Stripes<PTC, true> stripes;
-  typename Kv4Stripes<PTC, true>::Lane lanes = stripes.init(p, ratio);
+  typename Kv4Stripes<PTC, true>::Lane lanes = stripes.init(p, ratio, gridDim.y);
   const uint32_t end = (first + 1) * stripes.stripe;
   if (end >= stripes.total) return;
   Kv4Seq seq;
@@ -402,8 +416,8 @@ hipError_t launch_kv4_tree_wide(const Kv4AttendArgs& a, int D, int groups, bool 
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.target == 1) return e;
   // Many tiles of few parts: 32 channels a workgroup (16 trees of up to 64 nodes: 23 us with 8 to a
-  // workgroup, 15 with 32).  Few tiles of many parts: 8 (two trees of 13 nodes to 131072, 32 parts
-  // a tile: JOINFIG).
+  // workgroup, 15 with 32, when one XCD still had most of them).  Few tiles of many parts: 8 (two
+  // trees of 13 nodes to 131072, 32 parts a tile: 10 us).
   if (a.target >= 8 * a.tiles)
     hipLaunchKernelGGL(join_kernel<1>(D, bf), dim3(D / 8, a.target), dim3(256), 0, st, a);
   else
