@@ -1031,6 +1031,7 @@ int kv4_attention(const uint16_t* q, const int32_t* rows, const int32_t* lens,
   a.mask = mask;
   a.depth = depth;
   a.words = words;
+  a.part_shared = a.part_ml + (size_t)plan.slots * plan.cols * 2;
   return launched(
       launch_kv4_attend(plan, a, head, head / group, dtype == W4A16_DT_BF16, st));
 }

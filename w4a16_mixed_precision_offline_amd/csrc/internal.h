@@ -227,12 +227,14 @@ struct Kv4AttendArgs {
   const uint32_t* mask;  // of the nodes of trees, `words` a token; NULL: causal attention
   const int* depth;      // of the nodes; not read without a window
   int words;
+  float* part_shared;    // tiles of 128 columns of trees: KV4_TREE_SHARED of each stripe
 };
 struct Kv4AttendPlan {
   int cols;           // columns of a tile: 8, 16 (kv4_attention.hip) or 128 (kv4_prefill.hip)
   int col_tiles, target, chunk, chunks, slots, tiles;  // as in Kv4AttendArgs; slots 0: no chunks
   size_t floats, counters;  // workspace
 };
+constexpr int KV4_TREE_SHARED = 8;
 constexpr int KV4_STRIPES = 512;  // most stripes of a launch, and the wide tiles' target
 // workspace of any plan whose tiles have at most that many columns
 size_t kv4_attend_most_floats(int cols, int D);

@@ -567,10 +567,9 @@ AttendFn attend_kernel(int cols, bool bf, int D, int groups) {
 // 2 us in one of 128, a tile costs 10 and 4 blocks more, and tiles of 128 take 11 us more to hand
 // over and join; of several sequences the lengths are taken for half of what they may be.  16
 // against 128, 64 query heads on 8, us: 128 columns, contexts to 8 x 8192 / 1 x 32768 / 32 x 2048 /
-// 64 x 300 / 1 x 1000 tokens 64 / 60 / 74 / 59 / 13 against 56 / 52 / 52 / 33 / 20; 96 columns, 8 x
-// 8192 / 32 x 2048 / 1 x 32768: 41 / 55 / 55 against 47 / 46 / 49; 104 columns, 2 x 131072: 289
-// against 217; 64 columns, 8 x 8192 / 4 x 131072: 40 / 246 against 51 / 295; 512 columns, 1 x 4000:
-// 41 against 35.
+// 64 x 300 tokens 69 / 60 / 75 / 58 against 57 / 58 / 60 / 31; 96 columns, 8 x 8192 / 32 x 2048:
+// 41 / 55 against 47 / 50; 104 columns, 2 x 131072: 250 against 163; 256 columns, 8 x 8192: 126
+// against 96; 512 columns, 1 x 4000: 41 against 40; 64 columns, 4 x 131072: 248 against 287.
 bool wide_tree(int batch, long long columns, int max_new, int max_len, int heads, int window) {
   double span = (max_len + 31.0) / 32;
   if (batch > 1) span /= 2;
@@ -586,7 +585,7 @@ bool wide_tree(int batch, long long columns, int max_new, int max_len, int heads
 
 size_t kv4_attend_most_floats(int cols, int D) {
   // two slots a stripe of narrow tiles; fewer than target + target chunks of wide ones
-  return (size_t)2 * KV4_STRIPES * cols * (D + 2);
+  return (size_t)2 * KV4_STRIPES * cols * (D + 2) + (cols == 128 ? KV4_STRIPES * KV4_TREE_SHARED : 0);
 }
 
 Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, int q_heads,
@@ -627,9 +626,9 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     // on 8 kv heads 9.5 / 10.2 / 11.7 / 11.5, of 4000 13.8 / 11.6 / 11.8 / 14.8, of 16000 25.4 /
     // 25.9 / 16.5 / 16.6; six to 4000 15.9 / 15.2 / 12.5 / 15.3, to 16000 26 each; 24 to 1000
     // 16.1 / 16.1 / 16.0 / 12.5, to 16000 55 each.
-    // Tiles of 128 columns (trees), 4 / 8 / 16: 512 columns over 4000 tokens 38 / 35 / 37, 128 over
-    // 4000 21 / 22 / 32, over 32768 52 / 52 / 51.
-    p.chunk = 8;
+    // Tiles of 128 columns (trees), 8 / 12 / 16 / 24: 128 columns over 1 x 32768 tokens 58 / 58 / 59 /
+    // 63, 8 x 8192 57 / 57 / 58 / 62, 64 x 300 39 / 31 / 31 / 32; 512 over 1 x 4000 41 / 40 / 43 / 47.
+    p.chunk = p.cols == 128 ? 12 : 8;
     long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
     const bool wide = p.cols == 128;  // trees only: always stripes
     if (!wide && (batch > 1024 || stripes <= tiles)) return p;
@@ -641,6 +640,7 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     else if (stripes == 1) p.slots = 0;  // nothing to join
   }
   p.floats = (size_t)p.slots * p.cols * (D + 2);
+  if (tree && p.cols == 128 && p.slots) p.floats += (size_t)p.target * KV4_TREE_SHARED;
   return p;
 }
 

@@ -30,6 +30,14 @@ namespace {
 
 constexpr int WS = 2;  // blocks of a stage
 
+// What a stripe says of the tile that starts in it and goes on in others: `last` is the last of
+// them, 0 if there is no such tile.
+struct Shared {
+  int first, n, head, tile;
+  uint32_t last;
+};
+static_assert(sizeof(Shared) <= KV4_TREE_SHARED * sizeof(float), "it fits the workspace");
+
 template <int D, int NG>
 struct TreeStage {
   u32x4v k[WS][D / 16][64];
@@ -70,6 +78,9 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
   uint32_t place = blockIdx.x * stripes.stripe;
   const uint32_t stop =
       place + stripes.stripe < stripes.total ? place + stripes.stripe : stripes.total;
+  Shared* shared = reinterpret_cast<Shared*>(p.part_shared) + blockIdx.x;
+  const bool tells = p.slots && threadIdx.x == 0;
+  if (tells) shared->last = 0;
   for (bool again = false; place < stop; again = true) {
     Kv4Seq seq;
     int b, head, tile, span;
@@ -83,6 +94,8 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
     const uint32_t r1 = stop - u0 < (uint32_t)span ? stop - u0 : (uint32_t)span;
     if (r0 >= r1) continue;  // what rounds a tile up to whole stripes
     const bool last_part = r1 == (uint32_t)span;
+    if (r0 == 0 && !last_part && tells)
+      *shared = Shared{seq.first, seq.n, head, tile, (u0 + span - 1) / stripes.stripe};
     const Kv4Range rg = kv4_range<PTC, true>(p, seq, tile, ratio, r0, last_part ? -1 : (int)r1);
     const int b1 = rg.blk1;
     // every column sees the tokens [all_lo, rg.from)
@@ -345,26 +358,17 @@ __global__ __launch_bounds__(256) void kv4_tree_join_kernel(Kv4AttendArgs p) {
   const int c = lane & 31, h = lane >> 5, t = blockIdx.x * KN / 4, k0 = blockIdx.x * KN % 4;
   const uint32_t first = blockIdx.y;
   const int ratio = p.q_heads / p.heads;
-  Kv4Stripes<PTC, true> stripes;
-  typename Kv4Stripes<PTC, true>::Lane lanes = stripes.init(p, ratio, gridDim.y);
-  const uint32_t end = (first + 1) * stripes.stripe;
-  if (end >= stripes.total) return;
-  Kv4Seq seq;
-  int b, head, tile, span;
-  uint32_t u0;
-  stripes.find(p, end - 1, ratio, lanes, seq, b, head, tile, span, u0);
-  u0 += stripes.lead;
-  if (u0 / stripes.stripe != first || u0 + span <= end) return;
-  const uint32_t last = (u0 + span - 1) / stripes.stripe;
-  const int col = tile * PTC + 32 * wave + c, ci = col / ratio;
-  if (ci >= seq.n) return;
-  const int qh = head * ratio + col % ratio, row = seq.first + ci;
+  const Shared x = reinterpret_cast<const Shared*>(p.part_shared)[first];
+  if (x.last == 0) return;
+  const int col = x.tile * PTC + 32 * wave + c, ci = col / ratio;
+  if (ci >= x.n) return;
+  const int qh = x.head * ratio + col % ratio, row = x.first + ci;
   float m = kKv4None, l = 0.f;
   f32x4 o[KN];
 #pragma unroll
   for (int k = 0; k < KN; ++k) o[k] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 16 / KN
-  for (uint32_t i = first; i <= last; ++i) {
+  for (uint32_t i = first; i <= x.last; ++i) {
     const size_t slot = 2 * (size_t)i + (i == first);
     const float* ml = p.part_ml + (slot * PTC + 32 * wave + c) * 2;
     const f32x4* at = reinterpret_cast<const f32x4*>(p.part_o + slot * PTC * D) +
