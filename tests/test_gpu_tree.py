@@ -368,3 +368,26 @@ def test_pages_past_4_gib(lib, ratio, most):
     lib.w4a16_kv4_tree_attention(s.q.cuda(), s.dev[0], s.dev[1], table, big, s.dev[4], None, o, l, 2, s.tokens, s.max_new, most or s.max_len, s.words,
                                  w + 8, w + 16, 8 * ratio, 8, 128, 64, 64, pages, s.width, 0, 128 ** -0.5)
     assert torch.equal(o[:, :w], out[:, :w]) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_call_covers_the_captures_of_others(lib, D):
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    s = Trees([(2, 9)], 1, 1, D, 64, 32, F16, seed=15)
+    s.masks()
+    s.run(lib, stream=side)
+    for spread, heads, ratio, most in (([(40, 900)], 2, 4, None), ([(60, 900), (33, 200)], 2, 16, 60000), ([(7, 900)], 4, 1, 4000)):
+        s = Trees(spread, heads, ratio, D, 64, 64, F16, seed=16)
+        s.masks()
+        out, lse = s.run(lib, most)
+        q, w = s.q.cuda(), heads * ratio * D
+        o, l = torch.zeros_like(out), torch.zeros_like(lse)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            s.call(o, l, q, side)  # refused if the stream holds too little
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o[:, :w], out[:, :w]) and torch.equal(l, lse)

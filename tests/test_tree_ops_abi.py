@@ -52,6 +52,8 @@ def test_tree_refusals(code, change):
     *[(ALIGN, {n: MIS}) for n in ("q", "out", "lse", "mask", "depth")],
     (SHAPE, dict(words=1)), (SHAPE, dict(words=0)), (SHAPE, dict(max_new=41)), (SHAPE, dict(ldq=504)), (SHAPE, dict(ldo=516)),
     (SHAPE, dict(q_heads=0)), (SHAPE, dict(q_heads=5, kv_heads=2)), (SHAPE, dict(max_len=0)), (SHAPE, dict(max_len=(1 << 30) + 1)),
+    (SHAPE, dict(batch=4097, kv_heads=16384, q_heads=16384, ldq=1 << 21, ldo=1 << 21)),
+    (SHAPE, dict(batch=1024, tokens=1 << 20, max_new=1 << 19, words=1 << 14)),
     (SHAPE, dict(window=-1)), (ARG, dict(scale=0.0)), (ARG, dict(scale=float("nan"))), (ARG, dict(dtype=2))])
 def test_tree_attention_refusals(code, change):
     refused(w4.w4a16_kv4_tree_attention, code, *{**ATTEND, **change}.values())

@@ -959,6 +959,11 @@ bool kv4_attend_shape_ok(int batch, int tokens, int max_new, int max_len, int q_
       q_heads % kv_heads != 0 || (head != 64 && head != 128) || window < 0)
     return false;
   if ((long long)max_new * (q_heads / kv_heads) > (1LL << 30)) return false;
+  // rows may overlap, so that every sequence can have max_new nodes: all their tiles, with what a
+  // tile counts beside its blocks, stay below 2^32 in the division between workgroups
+  if (tree && ((long long)batch * kv_heads > (1LL << 26) ||
+               (long long)max_new * q_heads > (1LL << 30) / batch))
+    return false;
   const Kv4AttendPlan p =
       kv4_attend_plan(batch, tokens, max_new, max_len, q_heads, kv_heads, head, window, tree);
   return (long long)p.col_tiles <= (1LL << 30) / kv_heads / batch &&

@@ -27,6 +27,9 @@
 // the tokens that no column sees: what a page holds there may be anything.
 // A column that sees nothing gives 0 and a log-sum of -infinity.
 //
+// TREE: the new tokens are the nodes of a drafted tree, and what a column sees of the last
+// blocks is 32 bits that its node's mask gives for them; everything before the tree is as above.
+//
 // The blocks of all tiles are cut into equal stripes, one for each of the workgroups that
 // the card holds at once; the sums of a tile that stripes share are joined in order.
 //
@@ -42,7 +45,8 @@
 // against 57 us on the first.
 // Registers: 193 to 227 with 128 channels, two waves to a SIMD.  With groups of 32 the two
 // blocks and their s and m do not fit into 256: 17 are spilled in tiles of 8, 41 to 45 in tiles
-// of 16.  56 to 84 scalar registers of the division into stripes lie in vector registers.
+// of 16.  TREE: 167 to 241, with groups of 32 41 to 50 spilled; 26 nodes and 2000 tokens of 32 heads
+// (two tiles a head) 16.5 us.  56 to 84 scalar registers of the division into stripes lie in vector registers.
 #include "kv4_attend.h"
 
 namespace w4a16 {
@@ -632,6 +636,10 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
     const bool wide = p.cols == 128;  // trees only: always stripes
     if (!wide && (batch > 1024 || stripes <= tiles)) return p;
+    // Trees, tiles of 16: 32 parts of a tile at most, which one workgroup joins.  16 / 32 / 48 / 64 /
+    // no limit: 9 nodes over 36083 tokens, 8 heads on 1, 32 / 29 / 30 / 35 / 55; 16 over 100000
+    // 59 / 44 / 54 / 54 / 55; 4 over 100000, 16 on 2, 59 / 43 / 41 / 41 / 74.
+    if (tree && !wide && stripes > 32 * tiles) stripes = 32 * tiles;
     if (stripes > KV4_STRIPES) stripes = KV4_STRIPES;
     p.target = (int)stripes;
     p.tiles = tiles < (1 << 24) ? (int)tiles : 1 << 24;

@@ -13,10 +13,11 @@
 // of alternating phases, two waves to a SIMD: 644 ns where 432 and 360 are the parts).  Tiles
 // all full and of equal length (16 sequences of 64 nodes and 8192 tokens, 64 query heads on 8 of
 // 128 channels, groups of 64): 275 GFLOP in 500 us, 0.55 PFLOP/s (bf16 rows 403 us; groups of 128
-// 477 us; a large fp16 product runs at 1.16).  Parts of it left out: the second part of p 100 us,
-// LDS reads 93, unpacking and its loads 85, exponentials and sums 38; one workgroup to a compute
-// unit instead of two 707.  32 to 64 nodes and up to 8192 tokens: 100 GFLOP in 216 us, of which 5
-// join the parts; two trees of 13 nodes, contexts of 131072 and less, groups of 32: 157 us.
+// 477 us; a large fp16 product runs at 1.16).  Left out, of 513 us, the second part of p is worth
+// 100 us, LDS reads 93, unpacking and its loads 85, exponentials and sums 38; one workgroup to a
+// compute unit instead of two takes 707.  32 to 64 nodes and up to 8192 tokens: 100 GFLOP in 229
+// us, of which 13 join 67 MB of parts; two trees of 13 nodes, contexts of 131072 and less, groups
+// of 32: 162 us.
 // Registers: 234 with groups of 64 (places in LDS and in the pages are worked out again for each
 // stage: kept, they made 256 and spills).  2 are spilled with groups of 32.
 // Measured, not kept: 8 waves of 32 columns over one stage (478 us where 513, but half-empty tiles
@@ -419,9 +420,8 @@ hipError_t launch_kv4_tree_wide(const Kv4AttendArgs& a, int D, int groups, bool 
                      dim3(a.target), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.target == 1) return e;
-  // Many tiles of few parts: 32 channels a workgroup (16 trees of up to 64 nodes: 23 us with 8 to a
-  // workgroup, 15 with 32, when one XCD still had most of them).  Few tiles of many parts: 8 (two
-  // trees of 13 nodes to 131072, 32 parts a tile: 10 us).
+  // Many tiles of few parts: 32 channels a workgroup, few of many: 8.  8 against 32: 384 tiles of
+  // 2 or 3 parts 17 against 13 us, 16 tiles of 32 parts 13 against 18.
   if (a.target >= 8 * a.tiles)
     hipLaunchKernelGGL(join_kernel<1>(D, bf), dim3(D / 8, a.target), dim3(256), 0, st, a);
   else
