@@ -8,11 +8,13 @@
 // by 0.03 radians).  A token's angles serve all its heads, so a workgroup makes them once, one
 // thread an angle, and keeps cosines and sines in LDS.
 //
-// An item is 8 pairs of one head (two loads of 16 bytes), or 16 channels that are only copied.
+// An item is 8 pairs of one head, or 16 channels that are only copied: two runs of 8 channels, half
+// of the turned (copied) channels apart, so that the lanes of a load or store lie side by side
+// (neighbouring runs instead: 114 us where 110 below).
 //
 // Bound: HBM for prompts, latency for single tokens.  16384 tokens of 64 + 8 heads of 128
-// channels, half of them turned, into other rows: 604 MB in 123 us, 4.9 TB/s, the rate of a large
-// copy; 5041 of 40 + 8, three axes: 27 us; one token 2.3 us.
+// channels, half of them turned, into other rows: 604 MB in 110 us, 5.5 TB/s (a large copy: 4.85);
+// 5041 of 40 + 8, three axes: 124 MB in 21.5 us; one token 2.3 us.
 #include "internal.h"
 #include "rows16.h"
 
@@ -23,8 +25,8 @@ namespace {
 constexpr int RT = 256;     // threads of a workgroup
 constexpr int RU = 4;       // items of a thread with loads in flight
 
-// Grid: (tokens, pieces of a token's items).
-template <bool BF, bool NEIGHBOURS>
+// Grid: (tokens, pieces of a token's items).  PAST: stores go past the caches.
+template <bool BF, bool NEIGHBOURS, bool PAST>
 __global__ __launch_bounds__(RT) void rotary_kernel(RotaryArgs p) {
   extern __shared__ float turned[];  // [rot / 2] cosines, then sines
   const int half = p.rot / 2;
@@ -47,11 +49,12 @@ __global__ __launch_bounds__(RT) void rotary_kernel(RotaryArgs p) {
     x.item = u - h * p.items_head;
     int c;
     if (x.item < turns) {
-      c = NEIGHBOURS ? 16 * x.item : 8 * x.item;
-      x.second = NEIGHBOURS ? 8 : half;
+      c = 8 * x.item;
+      x.second = half;
     } else {
-      c = 16 * x.item;  // = rot + 16 (item - rot / 16)
-      x.second = c + 16 <= p.head ? 8 : 0;
+      const int apart = 8 * (p.items_head - turns);
+      c = p.rot + 8 * (x.item - turns);
+      x.second = c + apart < p.head ? apart : 0;
     }
     const bool is_k = h >= (unsigned)p.q_heads;
     const size_t at = (size_t)(is_k ? h - p.q_heads : h) * p.head + c;
@@ -91,15 +94,15 @@ __global__ __launch_bounds__(RT) void rotary_kernel(RotaryArgs p) {
     for (int i = 0; i < RU; ++i) {
       if (u0 + i * RT >= end) break;
       if (it[i].item < turns) {
-        const float* c = cosines + 8 * it[i].item;
-        const float* s = sines + 8 * it[i].item;
+        // neighbours: pairs 4 item .. + 3 of the first run, and half a head's pairs on of the second
+        const int at = NEIGHBOURS ? 4 * it[i].item : 8 * it[i].item, on = NEIGHBOURS ? half / 2 : 4;
         float x[8], y[8], cs[8], sn[8];
         unpack8<BF>(a[i], x);
         unpack8<BF>(b[i], y);
 #pragma unroll
         for (int e = 0; e < 8; e += 4) {
-          const f32x4 cc = *reinterpret_cast<const f32x4*>(c + e);
-          const f32x4 ss = *reinterpret_cast<const f32x4*>(s + e);
+          const f32x4 cc = *reinterpret_cast<const f32x4*>(cosines + at + (e ? on : 0));
+          const f32x4 ss = *reinterpret_cast<const f32x4*>(sines + at + (e ? on : 0));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             cs[e + j] = cc[j];
@@ -125,14 +128,27 @@ __global__ __launch_bounds__(RT) void rotary_kernel(RotaryArgs p) {
         a[i] = pack8<BF>(v);
         b[i] = pack8<BF>(w);
       }
-      *reinterpret_cast<u32x4v*>(it[i].dst) = a[i];
-      if (it[i].second) *reinterpret_cast<u32x4v*>(it[i].dst + it[i].second) = b[i];
+      u32x4v* first = reinterpret_cast<u32x4v*>(it[i].dst);
+      u32x4v* second = reinterpret_cast<u32x4v*>(it[i].dst + it[i].second);
+      if constexpr (PAST) {
+        __builtin_nontemporal_store(a[i], first);
+        if (it[i].second) __builtin_nontemporal_store(b[i], second);
+      } else {
+        *first = a[i];
+        if (it[i].second) *second = b[i];
+      }
     }
   };
   for (unsigned u = u0; u < end; u += RU * RT) {
     if (u != u0) load(u);
     store(u);
   }
+}
+
+typedef void (*RotaryFn)(RotaryArgs);
+template <bool BF, bool PAST>
+RotaryFn rotary_kernel_of(bool neighbours) {
+  return neighbours ? rotary_kernel<BF, true, PAST> : rotary_kernel<BF, false, PAST>;
 }
 
 }  // namespace
@@ -151,8 +167,14 @@ hipError_t launch_rotary(const RotaryArgs& args, bool neighbours, bool bf, hipSt
   a.piece = a.tokens <= 512 ? RT : a.items;
   const dim3 grid(a.tokens, (a.items + a.piece - 1) / a.piece);
   const size_t lds = (size_t)a.rot * sizeof(float);
-  const auto fn = bf ? (neighbours ? rotary_kernel<true, true> : rotary_kernel<true, false>)
-                     : (neighbours ? rotary_kernel<false, true> : rotary_kernel<false, false>);
+  // Stores past the caches where a run of lanes fills whole lines of 128 bytes: 5041 tokens of 40 + 8
+  // heads of 128 channels 21.5 us instead of 27.5; with half of each head turned (runs of 64
+  // bytes) 16384 tokens take 117 us that way and 110 the other.  What reads the rows next takes
+  // as long either way.
+  const bool lines = a.rot >= 128 && (a.items_head == a.rot / 16 || a.head - a.rot >= 128);
+  const bool past = a.tokens > 512 && lines;
+  const auto fn = bf ? (past ? rotary_kernel_of<true, true>(neighbours) : rotary_kernel_of<true, false>(neighbours))
+                     : (past ? rotary_kernel_of<false, true>(neighbours) : rotary_kernel_of<false, false>(neighbours));
   hipLaunchKernelGGL(fn, grid, dim3(RT), lds, st, a);
   return hipGetLastError();
 }
