@@ -636,6 +636,11 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
     const bool wide = p.cols == 128;  // trees only: always stripes
     if (!wide && (batch > 1024 || stripes <= tiles)) return p;
+    // Trees, tiles of 16 over short contexts: whole tiles where there are enough of them, since
+    // to share one costs as much as 16 blocks.  In stripes against whole, us: 3 trees of 93 nodes
+    // to 275 tokens, 64 query heads on 32, 37 / 29; 32 of 10 to 600, 64 on 8, 33 / 24; 64 of 4 to
+    // 500 29 / 22; 64 of 8 to 1000 49 / 46; 32 of 8 to 2048 44 / 46.
+    if (tree && !wide && tiles >= KV4_STRIPES && span <= 32) return p;
     // Trees, tiles of 16: 32 parts of a tile at most, which one workgroup joins.  16 / 32 / 48 / 64 /
     // no limit: 9 nodes over 36083 tokens, 8 heads on 1, 32 / 29 / 30 / 35 / 55; 16 over 100000
     // 59 / 44 / 54 / 54 / 55; 4 over 100000, 16 on 2, 59 / 43 / 41 / 41 / 74.
