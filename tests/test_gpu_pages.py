@@ -295,3 +295,33 @@ def test_layers_past_4_gib(lib):
     assert table.tolist() == [[ids[0], pages - 2]] and missing.item() == 0
     blocks = big.view(2, pages, heads, page // 32, -1)
     assert torch.equal(blocks[:, pages - 2, :, :2], blocks[:, ids[1], :, :2]) and (blocks[:, pages - 2, :, 2:] == 0).all()
+
+
+def test_fork_with_the_most_pages_in_a_graph(lib):
+    """2^19 pages need more LDS than a launch has unasked; one call serves a capture as well."""
+    heads, D, G, page, pages, W = 1, 64, 64, 32, 1 << 19, 3
+    pool = torch.zeros(pages * lib.w4a16_kv4_page_bytes(heads, D, G, page), dtype=torch.uint8, device="cuda")
+    pinned = torch.ones(pages, dtype=torch.uint8, device="cuda")
+    free = [7, 70000, 300001, pages - 1]
+    pinned[free] = 0
+    table, lens, parent, room = i32([[3, 9, -1], [3, pages - 2, -1]]), i32([40, 64]), i32([0, 0, 1]), i32([50, 70, 96])
+    out, held, missing = torch.zeros(3, W, dtype=torch.int32, device="cuda"), i32([0] * 3), i32([9])
+
+    def call(stream=None):
+        lib.w4a16_kv4_fork(pool, table, lens, parent, None, room, pinned, out, held, missing, 2, 3, 1, pool.numel(), heads, D, G, page, pages, W, stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(side)
+    # page 9 is pinned, so both rows copy it
+    for _ in range(3):
+        out.fill_(5)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert out.tolist() == [[3, 7, -1], [3, 70000, 300001], [3, pages - 2, pages - 1]] and held.tolist() == [40, 40, 64] and missing.item() == 0
+    pinned[9] = 0
+    call()
+    assert out.tolist() == [[3, 9, -1], [3, 7, 70000], [3, pages - 2, 300001]]
