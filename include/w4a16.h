@@ -526,8 +526,12 @@ size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len
  *   table_out (device, out) int32 [batch_out][width]: -1 where there is no page; lens_out (device,
  *     out) int32 [batch_out]: the tokens kept.  Neither may overlap table or lens.
  *   missing (device, out) int32 [1], may be NULL: how many pages there were too few; the last
- *     entries that were due are -1 then, the kept tokens of a copied page among them.  The old
- *     table and its pages are as they were, so the call can be made again with fewer rows.
+ *     entries that were due are -1 then, the kept tokens of a copied page among them.  Of the old
+ *     rows what the new ones keep is as it was, so the call can be made again from the old table
+ *     with fewer of the same rows, or less kept or less room in them.  The rest of the old rows
+ *     (those that no new row goes on from, tokens past keep) was free in this call too, and copies
+ *     may have been written there: what is to outlive a call that runs short is kept by a row of
+ *     it, or pinned.
  *   Old rows must not list a page twice; keep and room are cut off at width * page tokens.
  *   batch_out <= 2048, pages <= 2^19; the pool is that of w4a16_kv4_compact. */
 int w4a16_kv4_tree(const int32_t* parent, const int32_t* rows, const int32_t* lens, uint32_t* mask,

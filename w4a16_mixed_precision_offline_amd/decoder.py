@@ -276,7 +276,9 @@ class Kv4Pool(torch.nn.Module):
         """Who has which pages in the next step (w4a16_kv4_fork): row r of the new table goes on from
         row parent[r] (below 0: from nothing), keeps keep[r] of its tokens (None: all) and has pages
         for room[r] tokens; pinned uint8 [pages] are not given out.  Returns table, lens and how many
-        pages were missing (int32 [1]); where that is above 0 the old table still holds."""
+        pages were missing (int32 [1]).  Where that is above 0 the old table still holds for what these
+        rows keep: call again with fewer of them, or with less kept or less room.  Pages that none of
+        them keeps and that are not pinned may have been written already."""
         if table.dim() != 2 or parent.dim() != 1 or parent.shape[0] < 1:
             raise ValueError("table must be [batch, width] and parent [rows]")
         n = parent.shape[0]
