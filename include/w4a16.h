@@ -533,7 +533,8 @@ size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len
  *     may have been written there: what is to outlive a call that runs short is kept by a row of
  *     it, or pinned.
  *   Old rows must not list a page twice; keep and room are cut off at width * page tokens.
- *   batch_out <= 2048, pages <= 2^19; the pool is that of w4a16_kv4_compact. */
+ *   batch_out <= 2048, batch_out * width <= 2^30, pages <= 2^19; the pool is that of
+ *   w4a16_kv4_compact. */
 int w4a16_kv4_tree(const int32_t* parent, const int32_t* rows, const int32_t* lens, uint32_t* mask,
                    int32_t* depth, int32_t* pos, int batch, int tokens, int max_new, int words,
                    int window, void* stream);

@@ -1133,7 +1133,9 @@ int w4a16_kv4_fork(void* cache, const int32_t* table, const int32_t* lens, const
   int rc = check_kv4(p16, 1, p4, batch, 1, 1, kv_heads, head, group, page, pages, width,
                      W4A16_DT_F16);
   if (rc) return rc;
+  // the kernel counts the pages that all rows ask for in 32 bits
   if (batch_out < 1 || batch_out > KV4_FORK_ROWS || pages > KV4_FORK_PAGES ||
+      (long long)batch_out * width > (1LL << 30) ||
       !kv4_layers_ok(layers, layer_bytes, kv_heads, head, group, page, pages))
     return W4A16_ERR_SHAPE;
   if (table_out == table || lens_out == lens) return W4A16_ERR_ARG;
