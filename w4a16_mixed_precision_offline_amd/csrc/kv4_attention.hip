@@ -634,7 +634,9 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     // 63, 8 x 8192 57 / 57 / 58 / 62, 64 x 300 39 / 31 / 31 / 32; 512 over 1 x 4000 41 / 40 / 43 / 47.
     p.chunk = p.cols == 128 ? 12 : 8;
     long long stripes = tiles * ((span + p.chunk - 1) / p.chunk);
-    const bool wide = p.cols == 128;  // trees only: always stripes
+    // Trees only, and always stripes: two at least, since one tile of twelve blocks is never worth
+    // 128 columns (wide_tree: 77 us of workgroups at most against 5640 at least).
+    const bool wide = p.cols == 128;
     if (!wide && (batch > 1024 || stripes <= tiles)) return p;
     // Trees, tiles of 16 over short contexts: whole tiles where there are enough of them, since
     // to share one costs as much as 16 blocks.  In stripes against whole, us: 3 trees of 93 nodes
@@ -650,10 +652,9 @@ Kv4AttendPlan kv4_attend_plan(int batch, int tokens, int max_new, int max_len, i
     p.tiles = tiles < (1 << 24) ? (int)tiles : 1 << 24;
     p.slots = 2 * (int)stripes;
     if (!wide) p.counters = (size_t)stripes;
-    else if (stripes == 1) p.slots = 0;  // nothing to join
   }
   p.floats = (size_t)p.slots * p.cols * (D + 2);
-  if (tree && p.cols == 128 && p.slots) p.floats += (size_t)p.target * KV4_TREE_SHARED;
+  if (tree && p.cols == 128) p.floats += (size_t)p.target * KV4_TREE_SHARED;
   return p;
 }
 

@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
   const uint32_t stop =
       place + stripes.stripe < stripes.total ? place + stripes.stripe : stripes.total;
   Shared* shared = reinterpret_cast<Shared*>(p.part_shared) + blockIdx.x;
-  const bool tells = p.slots && threadIdx.x == 0;
+  const bool tells = threadIdx.x == 0;
   if (tells) shared->last = 0;
   for (bool again = false; place < stop; again = true) {
     Kv4Seq seq;
@@ -419,7 +419,7 @@ hipError_t launch_kv4_tree_wide(const Kv4AttendArgs& a, int D, int groups, bool 
   hipLaunchKernelGGL(bf ? tree_kernel<true>(D, groups) : tree_kernel<false>(D, groups),
                      dim3(a.target), dim3(256), 0, st, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.target == 1) return e;
+  if (e != hipSuccess) return e;
   // Many tiles of few parts: 32 channels a workgroup, few of many: 8.  8 against 32: 384 tiles of
   // 2 or 3 parts 17 against 13 us, 16 tiles of 32 parts 13 against 18.
   if (a.target >= 8 * a.tiles)
