@@ -496,7 +496,8 @@ size_t w4a16_kv4_workspace_bytes(int batch, int tokens, int max_new, int max_len
  *   that its bits name, itself only if they do; bits of nodes that the sequence does not have, and
  *   nodes past the mask's words, are not seen.  Any bits are allowed, a causal row among them.
  *   depth is read with window > 0 only (else it may be NULL), and brought into 0 .. nodes - 1.
- *   A node that sees nothing gets out 0 and lse -infinity.  batch * max_new * q_heads <= 2^30,
+ *   A node that sees nothing gets out 0 and lse -infinity.  A NaN reaches the nodes that see its
+ *   token and no others (in values: the channels of its group).  batch * max_new * q_heads <= 2^30,
  *   batch * kv_heads <= 2^26.  Everything else is as there; the workspace is
  *   w4a16_kv4_tree_workspace_bytes, and one call before a capture covers all others of that head.
  * w4a16_kv4_compact: the tokens of the accepted nodes move to the front of the tree's place, in

@@ -324,6 +324,32 @@ __device__ __forceinline__ int kv4_tree_first(const Kv4AttendArgs& p, const Kv4S
   const long long first = (long long)(s.len - s.n) + d - p.window + 1;
   return first < 0 ? 0 : (int)first;
 }
+// TREE: a token that some columns of a tile see and others do not may hold NaN (a rejected branch
+// may not spoil the accepted one), and the matrix instruction makes 0 x NaN of it for the others.
+// A NaN is in s or m, and makes a whole group of the token's channels NaN: so s and m are cleared
+// and the columns that see the token get the group's NaN by themselves.
+//
+// Whether a word of two fp16 numbers may hold a NaN (infinities do no harm in being looked at).
+__device__ __forceinline__ uint32_t maybe_nan(uint32_t w) {
+  return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+}
+// The tokens, of the eight of lane group g, whose s or m is NaN, a bit each; their s and m become 0.
+__device__ __forceinline__ uint32_t clear_nan_tokens(u32x4v& s, u32x4v& m, int g) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int up = 16 * (e & 1);
+    const uint32_t a = s[e >> 1] >> up & 0x7FFFu, b = m[e >> 1] >> up & 0x7FFFu;
+    if (a > 0x7C00u || b > 0x7C00u) {
+      bits |= 1u << e;
+      s[e >> 1] &= ~(0xFFFFu << up);
+      m[e >> 1] &= ~(0xFFFFu << up);
+    }
+  }
+  // kv4_slot_token of each, with nothing that a compiler could keep for the next block
+  return (bits & 0x0Fu) << (4 * g) | (bits & 0xF0u) << (12 + 4 * g);
+}
+
 // TREE: which of the 32 tokens from t0 on node `row` sees, a bit each.
 __device__ __forceinline__ uint32_t kv4_tree_sees(const Kv4AttendArgs& p, const Kv4Seq& s, int row,
                                                   int first, int t0) {

@@ -29,6 +29,7 @@
 //
 // TREE: the new tokens are the nodes of a drafted tree, and what a column sees of the last
 // blocks is 32 bits that its node's mask gives for them; everything before the tree is as above.
+// In those blocks a NaN stays with the columns that see its token (clear_nan_tokens).
 //
 // The blocks of all tiles are cut into equal stripes, one for each of the workgroups that
 // the card holds at once; the sums of a tile that stripes share are joined in order.
@@ -45,7 +46,7 @@
 // against 57 us on the first.
 // Registers: 193 to 227 with 128 channels, two waves to a SIMD.  With groups of 32 the two
 // blocks and their s and m do not fit into 256: 17 are spilled in tiles of 8, 41 to 45 in tiles
-// of 16.  TREE: 167 to 241, with groups of 32 41 to 50 spilled; 26 nodes and 2000 tokens of 32 heads
+// of 16.  TREE: 163 to 238, with groups of 32 29 to 48 spilled; 26 nodes and 2000 tokens of 32 heads
 // (two tiles a head) 16.5 us.  56 to 84 scalar registers of the division into stripes lie in vector registers.
 #include "kv4_attend.h"
 
@@ -305,21 +306,39 @@ __global__ __launch_bounds__(64 * AW, 2) void kv4_attend_kernel(Kv4AttendArgs p)
 #pragma unroll
         for (int off = 1; off < TC; off <<= 1) any |= (uint32_t)__shfl_xor((int)any, off);
       }
+      // (TREE: bits of the lane's tokens, kv4_slot_token, at places that all lanes have alike)
+      const uint32_t mine = sees >> (TC == 8 ? 4 * g + 2 * (r & 8) : 4 * g), some = any >> (4 * g);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int t = TC == 8 ? 4 * g + e + 2 * (r & 8) : kv4_slot_token(g, e);
-        if (TREE ? (sees >> t & 1u) == 0 : t0 + t < first || t0 + t > last) x[e] = -INFINITY;
+        if (TREE ? (mine >> kv4_slot_token(0, e) & 1u) == 0 : t0 + t < first || t0 + t > last)
+          x[e] = -INFINITY;
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int t = kv4_slot_token(g, e);
-        if (TREE ? (any >> t & 1u) == 0 : t0 + t < lo || t0 + t >= hi) {
+        if (TREE ? (some >> kv4_slot_token(0, e) & 1u) == 0 : t0 + t < lo || t0 + t >= hi) {
 #pragma unroll
           for (int q = 0; q < NG; ++q) {
             const uint32_t keep = e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
             kv.vs[q][e >> 1] &= keep;
             kv.vm[q][e >> 1] &= keep;
           }
+        }
+      }
+      if constexpr (TREE) {
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+          uint32_t odd = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) odd |= maybe_nan(kv.vs[q][i]) | maybe_nan(kv.vm[q][i]);
+          if (__ballot(odd != 0) == 0) continue;
+          uint32_t bits = clear_nan_tokens(kv.vs[q], kv.vm[q], g);
+          bits |= (uint32_t)__shfl_xor((int)bits, 16);
+          bits |= (uint32_t)__shfl_xor((int)bits, 32);
+          const float add = (sees & bits) != 0 ? NAN : 0.f;
+#pragma unroll
+          for (int t = q * NT / NG; t < (q + 1) * NT / NG; ++t) o[t] += add;
         }
       }
     }

@@ -7,7 +7,8 @@
 // a second kernel joins a tile's parts in their order.
 //
 // What each of a block's tokens is to each column is worked out once, by the waves that unpack the
-// block: 32 bits a column in LDS, where the block reaches into the tree or out of the window.
+// block: 32 bits a column in LDS, where the block reaches into the tree or out of the window;
+// there a NaN stays with the columns that see its token (clear_nan_tokens).
 //
 // Bound: matrix and vector instructions, of which the card overlaps two fifths at best (a probe
 // of alternating phases, two waves to a SIMD: 644 ns where 432 and 360 are the parts).  Tiles
@@ -18,8 +19,8 @@
 // compute unit instead of two takes 707.  32 to 64 nodes and up to 8192 tokens: 100 GFLOP in 229
 // us, of which 13 join 67 MB of parts; two trees of 13 nodes, contexts of 131072 and less, groups
 // of 32: 162 us.
-// Registers: 234 with groups of 64 (places in LDS and in the pages are worked out again for each
-// stage: kept, they made 256 and spills).  2 are spilled with groups of 32.
+// Registers: 236 with groups of 64 (places in LDS and in the pages are worked out again for each
+// stage: kept, they made 256 and spills).  4 are spilled with groups of 32.
 // Measured, not kept: 8 waves of 32 columns over one stage (478 us where 513, but half-empty tiles
 // of 256: 272 us where 250); K's operands read ahead of the block before, or of the unpacking, and
 // no barriers for the scheduler (no difference within 3%).
@@ -46,6 +47,7 @@ struct TreeStage {
   u32x4v m[WS][64];
   float s[WS][NG][32];
   uint32_t sees[WS][PTC];
+  uint32_t nans[WS][NG];  // tokens whose V is NaN in a group, of a block of kind 2
   int kind[WS];  // 0: nobody looks at it, 1: all columns see all of it, 2: `sees` says what
 };
 
@@ -119,6 +121,7 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[t][i] = 0.f;
     float ref = kKv4None, sum = 0.f;
+    uint32_t nan_groups = 0;  // groups of channels in which the column has seen a NaN
     bool far = false;  // of the whole wave: some column's reference is past kFar
 
     Piece<D, NG> piece;
@@ -165,6 +168,24 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
               piece.vm[i][e >> 1] &= keep;
             }
           }
+        constexpr int GH = Piece<D, NG>::GH;
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < GH; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) odd |= maybe_nan(piece.vs[i][j]) | maybe_nan(piece.vm[i][j]);
+        const bool look_close = __ballot(odd != 0) != 0;
+#pragma unroll
+        for (int i = 0; i < GH; ++i) {
+          uint32_t bits = 0;
+          if (look_close) {
+            bits = clear_nan_tokens(piece.vs[i], piece.vm[i], g);
+            bits |= (uint32_t)__shfl_xor((int)bits, 16);
+            bits |= (uint32_t)__shfl_xor((int)bits, 32);
+          }
+          // (with one group both waves of a block have it, and say the same)
+          if (lane == 0) st.nans[mine][(NG >= 2 ? half * GH : 0) + i] = bits;
+        }
       }
       // K: token 16 half + r, channels 32 j + 8 g ..
 #pragma unroll
@@ -225,6 +246,12 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if ((sees >> (8 * (i >> 2) + (i & 3)) & 1u) == 0) x[i] = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+          const uint32_t nans = __builtin_amdgcn_readfirstlane(st.nans[i_blk][q]);
+          if (nans == 0) continue;
+          if ((st.sees[i_blk][32 * wave + c] & nans) != 0) nan_groups |= 1u << q;
+        }
       }
       float top = max3(x[0], x[1], x[2]);
 #pragma unroll
@@ -313,6 +340,10 @@ __global__ __launch_bounds__(256, 2) void kv4_tree_wide_kernel(Kv4AttendArgs p) 
       }
     }
 
+    if (__ballot(nan_groups != 0) != 0) {
+#pragma unroll
+      for (int t = 0; t < CT; ++t) o[t] += nan_groups >> (t * NG / CT) & 1u ? NAN : 0.f;
+    }
     sum += __shfl_xor(sum, 32);
     int col_ = tile * PTC + 32 * wave + c;
     asm volatile("" : "+v"(col_));  // worked out again rather than kept in registers
