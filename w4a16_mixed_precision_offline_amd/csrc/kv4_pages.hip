@@ -419,10 +419,12 @@ hipError_t launch_kv4_fork(const Kv4ForkArgs& a, int D, int groups, hipStream_t 
   int slots = 64;
   while (slots < 2 * a.rows) slots *= 2;
   const size_t lds = ((a.pages + 31) / 32 + 2 * slots + 3 * a.rows + FT) * sizeof(int);
+  constexpr int most = (KV4_FORK_PAGES / 32 + 4 * KV4_FORK_ROWS + 3 * KV4_FORK_ROWS + FT) * sizeof(int);
   hipError_t e = hipSuccess;
+  // the same for every call, since another thread's smaller one may come between this and the launch
   if (lds > 65536)
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(kv4_fork_kernel),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+                            hipFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kv4_fork_kernel, dim3(1), dim3(FT), lds, st, a, slots);
   if ((e = hipGetLastError()) != hipSuccess) return e;
