@@ -230,7 +230,8 @@ struct Kv4AttendArgs {
   float* part_shared;    // tiles of 128 columns of trees: KV4_TREE_SHARED of each stripe
 };
 struct Kv4AttendPlan {
-  int cols;           // columns of a tile: 8, 16 (kv4_attention.hip) or 128 (kv4_prefill.hip)
+  int cols;           // columns of a tile: 8, 16 (kv4_attention.hip) or 128 (kv4_prefill.hip, trees:
+                      // kv4_tree_wide.hip)
   int col_tiles, target, chunk, chunks, slots, tiles;  // as in Kv4AttendArgs; slots 0: no chunks
   size_t floats, counters;  // workspace
 };

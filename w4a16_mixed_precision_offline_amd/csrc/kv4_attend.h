@@ -1,5 +1,5 @@
-// What the two attention kernels over the 4-bit cache share: operands made from codes, and
-// which workgroup does which part (kv4_attention.hip, kv4_prefill.hip).
+// What the attention kernels over the 4-bit cache share: operands made from codes, and which
+// workgroup does which part (kv4_attention.hip, kv4_prefill.hip, kv4_tree_wide.hip).
 #pragma once
 #include "kv4.h"
 

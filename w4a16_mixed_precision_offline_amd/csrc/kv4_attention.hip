@@ -593,6 +593,13 @@ AttendFn attend_kernel(int cols, bool bf, int D, int groups) {
 // 64 x 300 tokens 69 / 60 / 75 / 58 against 57 / 58 / 60 / 31; 96 columns, 8 x 8192 / 32 x 2048:
 // 41 / 55 against 47 / 50; 104 columns, 2 x 131072: 250 against 163; 256 columns, 8 x 8192: 126
 // against 96; 512 columns, 1 x 4000: 41 against 40; 64 columns, 4 x 131072: 248 against 287.
+// The rule has one price for all types, heads and groups (fp16, 128 channels, groups of 64).  The
+// others, 8 x 8192 tokens of 128 / 96 / 64 columns: bf16 51 / 46 / 51 against 44 / 48 / 54; groups of
+// 128 64 / 54 / 40 against 54 / 53 / 48; groups of 32 91 / 67 / 57 against 60 / 53 / 60, bf16 77 /
+// 72 / 61 against 50 / 55 / 56; 64 channels 45 / 31 / 25 against 40 / 38 / 32.  It is wrong by up to
+// 1.3 for groups of 32 and 96 columns, and by 1.1 for 64 channels, 512 columns over 1 x 4000 (29
+// against 31).  Nor does it count how long a tile is looked for among many sequences: 128 columns
+// of 2048 x 300 tokens 1725 against 1099, of 8192 x 150 6133 against 8275.
 bool wide_tree(int batch, long long columns, int max_new, int max_len, int heads, int window) {
   double span = (max_len + 31.0) / 32;
   if (batch > 1) span /= 2;

@@ -13,12 +13,12 @@
 // Bound: matrix and vector instructions, of which the card overlaps two fifths at best (a probe
 // of alternating phases, two waves to a SIMD: 644 ns where 432 and 360 are the parts).  Tiles
 // all full and of equal length (16 sequences of 64 nodes and 8192 tokens, 64 query heads on 8 of
-// 128 channels, groups of 64): 275 GFLOP in 500 us, 0.55 PFLOP/s (bf16 rows 403 us; groups of 128
-// 477 us; a large fp16 product runs at 1.16).  Left out, of 513 us, the second part of p is worth
+// 128 channels, groups of 64): 275 GFLOP in 483 us, 0.57 PFLOP/s (bf16 rows 401 us; groups of 128
+// 464 us; a large fp16 product runs at 1.16).  Left out, of 513 us, the second part of p is worth
 // 100 us, LDS reads 93, unpacking and its loads 85, exponentials and sums 38; one workgroup to a
-// compute unit instead of two takes 707.  32 to 64 nodes and up to 8192 tokens: 100 GFLOP in 229
+// compute unit instead of two takes 707.  32 to 64 nodes and up to 8192 tokens: 100 GFLOP in 225
 // us, of which 13 join 67 MB of parts; two trees of 13 nodes, contexts of 131072 and less, groups
-// of 32: 162 us.
+// of 32: 161 us.
 // Registers: 236 with groups of 64 (places in LDS and in the pages are worked out again for each
 // stage: kept, they made 256 and spills).  4 are spilled with groups of 32.
 // Measured, not kept: 8 waves of 32 columns over one stage (478 us where 513, but half-empty tiles

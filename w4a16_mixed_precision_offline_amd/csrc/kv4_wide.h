@@ -54,52 +54,52 @@ __device__ __forceinline__ void wide_queries(const Kv4AttendArgs& p, int row, in
                                              half8v* qf, half8v& qm, float& cf) {
   constexpr int J = D / 16, JG = J / NG;
   float top = 0.f;
-    u32x4v raw[J];
+  u32x4v raw[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      raw[j] = *reinterpret_cast<const u32x4v*>(p.q + (size_t)row * p.ldq + (size_t)qh * D +
-                                                16 * j + 8 * h);
-      float f[8];
-      unpack8<BF>(raw[j], f);
+  for (int j = 0; j < J; ++j) {
+    raw[j] = *reinterpret_cast<const u32x4v*>(p.q + (size_t)row * p.ldq + (size_t)qh * D +
+                                              16 * j + 8 * h);
+    float f[8];
+    unpack8<BF>(raw[j], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+  }
+  top = fmaxf(top, __shfl_xor(top, 32));
+  const int d = query_exponent(top);
+  const float up = __builtin_ldexpf(1.f, d);
+  float qsum[NG];
+#pragma unroll
+  for (int q = 0; q < NG; ++q) qsum[q] = 0.f;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    float f[8], x[8];
+    unpack8<BF>(raw[j], f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = f[e] * up;
+      qsum[j / JG] += x[e];
+      if (e & 2) x[e] *= 0.0625f;
     }
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const int d = query_exponent(top);
-    const float up = __builtin_ldexpf(1.f, d);
-    float qsum[NG];
+    qf[j] = __builtin_bit_cast(half8v, pack8<false>(x));
+  }
+  // (sum q) / 2^8 of a group as three fp16 numbers: groups 0, 1 at channels 0..5 of the
+  // operand, groups 2, 3 at 8..13
+  float x[8];
 #pragma unroll
-    for (int q = 0; q < NG; ++q) qsum[q] = 0.f;
+  for (int e = 0; e < 8; ++e) x[e] = 0.f;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      float f[8], x[8];
-      unpack8<BF>(raw[j], f);
+  for (int q = 0; q < NG; ++q) {
+    float y = (qsum[q] + __shfl_xor(qsum[q], 32)) * 0x1p-8f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] = f[e] * up;
-        qsum[j / JG] += x[e];
-        if (e & 2) x[e] *= 0.0625f;
-      }
-      qf[j] = __builtin_bit_cast(half8v, pack8<false>(x));
+    for (int k = 0; k < 3; ++k) {
+      const float z = lo16<false>(to16<false>(y));
+      y -= z;
+      if (h == q / 2) x[3 * (q & 1) + k] = z;
     }
-    // (sum q) / 2^8 of a group as three fp16 numbers: groups 0, 1 at channels 0..5 of the
-    // operand, groups 2, 3 at 8..13
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-#pragma unroll
-    for (int q = 0; q < NG; ++q) {
-      float y = (qsum[q] + __shfl_xor(qsum[q], 32)) * 0x1p-8f;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const float z = lo16<false>(to16<false>(y));
-        y -= z;
-        if (h == q / 2) x[3 * (q & 1) + k] = z;
-      }
-    }
-    qm = __builtin_bit_cast(half8v, pack8<false>(x));
-    // above 0, which would make NaN of a masked logit; what is less leaves nothing of the others
-    cf = fmaxf(__builtin_ldexpf(p.scale * 1.4426950408889634f, 8 - d), 0x1p-126f);
+  }
+  qm = __builtin_bit_cast(half8v, pack8<false>(x));
+  // above 0, which would make NaN of a masked logit; what is less leaves nothing of the others
+  cf = fmaxf(__builtin_ldexpf(p.scale * 1.4426950408889634f, 8 - d), 0x1p-126f);
 }
 
 }  // namespace w4a16
